@@ -14,11 +14,14 @@ Functions mirror the C entry points:
     decode_paged   -> fa_decode_paged   (paged split-KV decode)
     fp8_prepare    -> fa_fp8_prepare    (Hadamard rotation + E4M3 operands)
     fwd_fp8        -> fa_fwd_fp8        (FP8 prefill on those operands)
+    cache_fork, cache_append, cache_copy_pages, cache_collect, cache_compact
+                   -> fa_cache_*        (the pages of the cache)
     decode_paged_noalloc, decode_workspace_bytes, bwd_workspace_bytes,
     check_device_error, selftest_watchdog, status_string, version
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -35,6 +38,7 @@ FA_ERR_ALIGNMENT = -3
 FA_ERR_WORKSPACE = -4
 FA_ERR_CUDA = -5
 FA_ERR_TIMEOUT = -6
+FA_ERR_PAGES = -7
 FA_OUT_BF16 = 0
 FA_OUT_FP32 = 1
 
@@ -44,6 +48,9 @@ EXPORTS = ("fa_fwd", "fa_fwd_varlen", "fa_fwd_sinks", "fa_fwd_varlen_sinks", "fa
            "fa_bwd_varlen_sinks",
            "fa_decode_workspace_bytes", "fa_decode_paged", "fa_decode_paged_sinks",
            "fa_decode_paged_fp8", "fa_fp8_workspace_bytes", "fa_fp8_prepare", "fa_fwd_fp8",
+           "fa_cache_fork", "fa_cache_append", "fa_cache_copy_pages",
+           "fa_cache_collect_workspace_bytes", "fa_cache_collect",
+           "fa_cache_compact_workspace_bytes", "fa_cache_compact",
            "fa_decode_paged_noalloc", "fa_status_string", "fa_check_device_error",
            "fa_selftest_watchdog", "fa_version")
 
@@ -103,6 +110,20 @@ def _load():
     lib.fa_decode_paged.restype = i
     lib.fa_decode_paged_noalloc.argtypes = [vp] * 7 + [i] * 7 + [f, vp]
     lib.fa_decode_paged_noalloc.restype = i
+    lib.fa_cache_fork.argtypes = [vp] * 4 + [i, vp, vp, i, vp, i] + [vp] * 5 + [i] * 5 + [vp]
+    lib.fa_cache_fork.restype = i
+    lib.fa_cache_append.argtypes = [vp] * 3 + [i, i] + [vp] * 8 + [i] * 5 + [vp]
+    lib.fa_cache_append.restype = i
+    lib.fa_cache_copy_pages.argtypes = [vp] * 4 + [i, vp, vp] + [i] * 5 + [vp]
+    lib.fa_cache_copy_pages.restype = i
+    lib.fa_cache_collect_workspace_bytes.argtypes = [i]
+    lib.fa_cache_collect_workspace_bytes.restype = sz
+    lib.fa_cache_collect.argtypes = [vp] * 2 + [i] * 4 + [vp] * 3 + [sz, vp]
+    lib.fa_cache_collect.restype = i
+    lib.fa_cache_compact_workspace_bytes.argtypes = [i]
+    lib.fa_cache_compact_workspace_bytes.restype = sz
+    lib.fa_cache_compact.argtypes = [vp] * 4 + [i, vp, vp, i] + [vp] * 3 + [i] * 5 + [vp, sz, vp]
+    lib.fa_cache_compact.restype = i
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_check_device_error.argtypes = [vp]
@@ -520,6 +541,181 @@ def decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, scale=None,
                                         _ptr(lse), S, P, Hq, Hkv, d, ps, maxp, float(scale),
                                         _stream(stream)), "fa_decode_paged_noalloc")
     return out, lse
+
+
+def _device_of(first, **others):
+    """A context in which the device of `first` is current; the others must be on it."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise FAError(FA_ERR_INVALID_ARG, f"{name} is on {t.device}, not {first.device}")
+    if first.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(first.device)
+
+
+def _need_cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks a paged cache and its scales; returns it with E4M3 values as uint8
+    codes, and the bytes of an element."""
+    if isinstance(k_cache, torch.Tensor) and k_cache.dtype == torch.float8_e4m3fn:
+        k_cache = k_cache.view(torch.uint8)
+    if isinstance(v_cache, torch.Tensor) and v_cache.dtype == torch.float8_e4m3fn:
+        v_cache = v_cache.view(torch.uint8)
+    dtype = k_cache.dtype if getattr(k_cache, "dtype", None) == torch.uint8 else torch.bfloat16
+    _need(k_cache, dtype, 4, "k_cache")
+    _need(v_cache, dtype, 4, "v_cache")
+    if v_cache.shape != k_cache.shape:
+        raise FAError(FA_ERR_INVALID_ARG, "v_cache shape")
+    if dtype == torch.uint8:
+        _need(k_scale, torch.float32, 2, "k_scale")
+        _need(v_scale, torch.float32, 2, "v_scale")
+        want = (k_cache.shape[0], k_cache.shape[2])
+        if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want:
+            raise FAError(FA_ERR_INVALID_ARG, "k_scale/v_scale shape")
+    elif k_scale is not None or v_scale is not None:
+        raise FAError(FA_ERR_INVALID_ARG, "scales with a bf16 cache")
+    return k_cache, v_cache, 1 if dtype == torch.uint8 else 2
+
+
+def _need_ints(shape, name, t):
+    _need(t, torch.int32, len(shape), name)
+    if tuple(t.shape) != tuple(shape):
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} shape {tuple(t.shape)}, not {tuple(shape)}")
+
+
+def _bytes_of(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise FAError(FA_ERR_WORKSPACE, "workspace must be a contiguous CUDA tensor")
+    return workspace
+
+
+def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, free_count,
+               block_table_out, seq_lens_out, free_count_out, k_scale=None, v_scale=None,
+               stream=None):
+    """The next batch of slots: slot i continues slot parents[i] (-1: empty), sharing full
+    pages and copying a partly filled last page for all but the first that continue it.
+    caches [P,16,Hkv,d] (bf16, or E4M3 with scales [P,Hkv]), block_table [S,maxp], seq_lens
+    [S], parents [N], free_pages [P], free_count [1] int32 -> writes block_table_out [N,maxp],
+    seq_lens_out [N], free_count_out [1], which must not overlap the inputs."""
+    k_cache, v_cache, eb = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    P, ps, Hkv, d = k_cache.shape
+    _need(block_table, torch.int32, 2, "block_table")
+    _need(parents, torch.int32, 1, "parents")
+    S, maxp = block_table.shape
+    N = parents.shape[0]
+    _need_ints((S,), "seq_lens", seq_lens)
+    _need_ints((P,), "free_pages", free_pages)
+    _need_ints((1,), "free_count", free_count)
+    _need_ints((N, maxp), "block_table_out", block_table_out)
+    _need_ints((N,), "seq_lens_out", seq_lens_out)
+    _need_ints((1,), "free_count_out", free_count_out)
+    with _device_of(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                    block_table=block_table, seq_lens=seq_lens, parents=parents,
+                    free_pages=free_pages, free_count=free_count, block_table_out=block_table_out,
+                    seq_lens_out=seq_lens_out, free_count_out=free_count_out):
+        _check(_lib.fa_cache_fork(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), eb,
+                                  _ptr(block_table), _ptr(seq_lens), S, _ptr(parents), N,
+                                  _ptr(free_pages), _ptr(free_count), _ptr(block_table_out),
+                                  _ptr(seq_lens_out), _ptr(free_count_out), P, Hkv, d, ps, maxp,
+                                  _stream(stream)), "fa_cache_fork")
+
+
+def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, free_pages,
+                 free_count, seq_lens_out, free_count_out, stream=None):
+    """New tokens behind the sequences' ends.  k_new, v_new [T,Hkv,d] bf16 packed by cu_new
+    [S+1]; caches [P,16,Hkv,d] bf16; block_table [S,maxp] (gets the pages taken), seq_lens
+    [S], free_pages [P], free_count [1] int32 -> writes seq_lens_out [S], free_count_out [1],
+    which must not be the inputs."""
+    _need(k_new, torch.bfloat16, 3, "k_new")
+    _need(v_new, torch.bfloat16, 3, "v_new")
+    _need(k_cache, torch.bfloat16, 4, "k_cache")
+    _need(v_cache, torch.bfloat16, 4, "v_cache")
+    P, ps, Hkv, d = k_cache.shape
+    T = k_new.shape[0]
+    if v_cache.shape != k_cache.shape or tuple(k_new.shape) != (T, Hkv, d) or v_new.shape != k_new.shape:
+        raise FAError(FA_ERR_INVALID_ARG, "k_new/v_new/v_cache shape")
+    _need(block_table, torch.int32, 2, "block_table")
+    S, maxp = block_table.shape
+    _need_ints((S + 1,), "cu_new", cu_new)
+    _need_ints((S,), "seq_lens", seq_lens)
+    _need_ints((P,), "free_pages", free_pages)
+    _need_ints((1,), "free_count", free_count)
+    _need_ints((S,), "seq_lens_out", seq_lens_out)
+    _need_ints((1,), "free_count_out", free_count_out)
+    with _device_of(k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new, cu_new=cu_new,
+                    block_table=block_table, seq_lens=seq_lens, free_pages=free_pages,
+                    free_count=free_count, seq_lens_out=seq_lens_out,
+                    free_count_out=free_count_out):
+        _check(_lib.fa_cache_append(_ptr(k_new), _ptr(v_new), _ptr(cu_new), S, T, _ptr(k_cache),
+                                    _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+                                    _ptr(free_pages), _ptr(free_count), _ptr(seq_lens_out),
+                                    _ptr(free_count_out), P, Hkv, d, ps, maxp, _stream(stream)),
+               "fa_cache_append")
+
+
+def cache_copy_pages(k_cache, v_cache, src, dst, k_scale=None, v_scale=None, stream=None):
+    """Page src[i] of the caches to page dst[i] (int32 [n], device), with its scales."""
+    k_cache, v_cache, eb = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    P, ps, Hkv, d = k_cache.shape
+    _need(src, torch.int32, 1, "src")
+    _need_ints(src.shape, "dst", dst)
+    with _device_of(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, src=src, dst=dst):
+        _check(_lib.fa_cache_copy_pages(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                        eb, _ptr(src), _ptr(dst), src.shape[0], P, Hkv, d, ps,
+                                        _stream(stream)), "fa_cache_copy_pages")
+
+
+def cache_collect_workspace_bytes(num_pages) -> int:
+    return int(_lib.fa_cache_collect_workspace_bytes(int(num_pages)))
+
+
+def cache_collect(block_table, seq_lens, free_pages, free_count, page_size=16, workspace=None,
+                  stream=None):
+    """The pages that no sequence uses, descending, into free_pages [P] and free_count [1]
+    (int32, device), from block_table [S,maxp] and seq_lens [S]."""
+    _need(block_table, torch.int32, 2, "block_table")
+    _need(free_pages, torch.int32, 1, "free_pages")
+    S, maxp = block_table.shape
+    P = free_pages.shape[0]
+    _need_ints((S,), "seq_lens", seq_lens)
+    _need_ints((1,), "free_count", free_count)
+    workspace = _bytes_of(workspace, cache_collect_workspace_bytes(P), block_table.device)
+    with _device_of(block_table, seq_lens=seq_lens, free_pages=free_pages, free_count=free_count,
+                    workspace=workspace):
+        _check(_lib.fa_cache_collect(_ptr(block_table), _ptr(seq_lens), S, maxp, P,
+                                     int(page_size), _ptr(free_pages), _ptr(free_count),
+                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _stream(stream)), "fa_cache_collect")
+
+
+def cache_compact_workspace_bytes(num_pages) -> int:
+    return int(_lib.fa_cache_compact_workspace_bytes(int(num_pages)))
+
+
+def cache_compact(k_cache, v_cache, block_table, seq_lens, block_table_out, free_pages, free_count,
+                  k_scale=None, v_scale=None, workspace=None, stream=None):
+    """Moves the pages in use to the cache's front.  caches [P,16,Hkv,d] (bf16, or E4M3 with
+    scales), block_table [S,maxp], seq_lens [S] int32 -> writes block_table_out [S,maxp] (may
+    be block_table), free_pages [P], free_count [1]."""
+    k_cache, v_cache, eb = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    P, ps, Hkv, d = k_cache.shape
+    _need(block_table, torch.int32, 2, "block_table")
+    S, maxp = block_table.shape
+    _need_ints((S,), "seq_lens", seq_lens)
+    _need_ints((S, maxp), "block_table_out", block_table_out)
+    _need_ints((P,), "free_pages", free_pages)
+    _need_ints((1,), "free_count", free_count)
+    workspace = _bytes_of(workspace, cache_compact_workspace_bytes(P), k_cache.device)
+    with _device_of(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                    block_table=block_table, seq_lens=seq_lens, block_table_out=block_table_out,
+                    free_pages=free_pages, free_count=free_count, workspace=workspace):
+        _check(_lib.fa_cache_compact(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                     eb, _ptr(block_table), _ptr(seq_lens), S,
+                                     _ptr(block_table_out), _ptr(free_pages), _ptr(free_count), P,
+                                     Hkv, d, ps, maxp, _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(),
+                                     _stream(stream)), "fa_cache_compact")
 
 
 def selftest_watchdog(stream=None) -> int:

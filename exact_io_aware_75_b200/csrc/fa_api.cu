@@ -602,6 +602,175 @@ int fa_fwd_fp8(const void *q8, const void *k8, const void *vt8, const float *q_s
     return map_rc(fa::launch_prefill_fp8(a, static_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// Sequences whose bookkeeping one block keeps in shared memory (32 KiB).
+constexpr int kMaxCacheSlots = 8192;
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+int check_cache(const void *k, const void *v, const float *ks, const float *vs, int elem_bytes,
+                int num_pages, int Hkv, int d, int page_size, int max_pages) {
+    if (num_pages < 0 || Hkv <= 0 || max_pages <= 0) return FA_ERR_INVALID_ARG;
+    if (elem_bytes != 1 && elem_bytes != 2) return FA_ERR_INVALID_ARG;
+    if (page_size != 16 || (d != 64 && d != 128) || Hkv > 65536) return FA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page_size > INT32_MAX / 2 ||
+        (long long)max_pages * page_size > INT32_MAX / 2)
+        return FA_ERR_UNSUPPORTED;
+    if (num_pages == 0 || !k || !v) return FA_ERR_INVALID_ARG;
+    // E4M3 codes come with both scales, bf16 values with none
+    if ((elem_bytes == 1) != (ks != nullptr) || (elem_bytes == 1) != (vs != nullptr))
+        return FA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned4(ks) || !aligned4(vs)) return FA_ERR_ALIGNMENT;
+    return FA_OK;
+}
+
+fa::CachePages cache_pages(void *k, void *v, float *ks, float *vs, int elem_bytes, int num_pages,
+                           int Hkv, int d) {
+    fa::CachePages c;
+    c.k = k; c.v = v; c.k_scale = ks; c.v_scale = vs;
+    c.num_pages = num_pages; c.Hkv = Hkv; c.d = d; c.elem_bytes = elem_bytes;
+    return c;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_cache_fork(void *k_cache, void *v_cache, float *k_scale, float *v_scale, int elem_bytes,
+                  const int *block_table, const int *seq_lens, int num_slots, const int *parents,
+                  int num_new, const int *free_pages, const int *free_count, int *block_table_out,
+                  int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
+                  int page_size, int max_pages_per_seq, void *stream) {
+    if (num_slots < 0 || num_new < 0) return FA_ERR_INVALID_ARG;
+    const int rc = check_cache(k_cache, v_cache, k_scale, v_scale, elem_bytes, num_pages, Hkv, d,
+                               page_size, max_pages_per_seq);
+    if (rc) return rc;
+    if (num_slots > kMaxCacheSlots || num_new > kMaxCacheSlots) return FA_ERR_UNSUPPORTED;
+    if (!free_pages || !free_count || !free_count_out) return FA_ERR_INVALID_ARG;
+    if (num_slots > 0 && (!block_table || !seq_lens)) return FA_ERR_INVALID_ARG;
+    if (num_new > 0 && (!parents || !block_table_out || !seq_lens_out)) return FA_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(parents) ||
+        !aligned4(free_pages) || !aligned4(free_count) || !aligned4(block_table_out) ||
+        !aligned4(seq_lens_out) || !aligned4(free_count_out))
+        return FA_ERR_ALIGNMENT;
+    const size_t row = (size_t)max_pages_per_seq * 4;
+    if (overlap(block_table, num_slots * row, block_table_out, num_new * row) ||
+        overlap(seq_lens, (size_t)num_slots * 4, seq_lens_out, (size_t)num_new * 4) ||
+        overlap(free_count, 4, free_count_out, 4))
+        return FA_ERR_INVALID_ARG;
+    return map_rc(fa::launch_cache_fork(
+        cache_pages(k_cache, v_cache, k_scale, v_scale, elem_bytes, num_pages, Hkv, d), block_table,
+        seq_lens, num_slots, parents, num_new, free_pages, free_count, block_table_out,
+        seq_lens_out, free_count_out, max_pages_per_seq, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_cache_append(const void *k_new, const void *v_new, const int *cu_new, int num_seqs,
+                    int total_new, void *k_cache, void *v_cache, int *block_table,
+                    const int *seq_lens, const int *free_pages, const int *free_count,
+                    int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
+                    int page_size, int max_pages_per_seq, void *stream) {
+    if (num_seqs < 0 || total_new < 0 || (num_seqs == 0 && total_new > 0)) return FA_ERR_INVALID_ARG;
+    const int rc = check_cache(k_cache, v_cache, nullptr, nullptr, 2, num_pages, Hkv, d, page_size,
+                               max_pages_per_seq);
+    if (rc) return rc;
+    if (num_seqs > kMaxCacheSlots || total_new > INT32_MAX / 2) return FA_ERR_UNSUPPORTED;
+    if (!free_pages || !free_count || !free_count_out) return FA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!cu_new || !block_table || !seq_lens || !seq_lens_out))
+        return FA_ERR_INVALID_ARG;
+    if (total_new > 0 && (!k_new || !v_new)) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(cu_new) || !aligned4(block_table) ||
+        !aligned4(seq_lens) || !aligned4(free_pages) || !aligned4(free_count) ||
+        !aligned4(seq_lens_out) || !aligned4(free_count_out))
+        return FA_ERR_ALIGNMENT;
+    if (overlap(seq_lens, (size_t)num_seqs * 4, seq_lens_out, (size_t)num_seqs * 4) ||
+        overlap(free_count, 4, free_count_out, 4))
+        return FA_ERR_INVALID_ARG;
+    return map_rc(fa::launch_cache_append(
+        cache_pages(k_cache, v_cache, nullptr, nullptr, 2, num_pages, Hkv, d), k_new, v_new, cu_new,
+        num_seqs, total_new, block_table, seq_lens, free_pages, free_count, seq_lens_out,
+        free_count_out, max_pages_per_seq, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_cache_copy_pages(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                        int elem_bytes, const int *src, const int *dst, int n, int num_pages,
+                        int Hkv, int d, int page_size, void *stream) {
+    if (n < 0) return FA_ERR_INVALID_ARG;
+    const int rc = check_cache(k_cache, v_cache, k_scale, v_scale, elem_bytes, num_pages, Hkv, d,
+                               page_size, 1);
+    if (rc) return rc;
+    if (n == 0) return FA_OK;
+    if (!src || !dst) return FA_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(dst)) return FA_ERR_ALIGNMENT;
+    return map_rc(fa::launch_cache_copy(
+        cache_pages(k_cache, v_cache, k_scale, v_scale, elem_bytes, num_pages, Hkv, d), src, dst, n,
+        static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_cache_collect_workspace_bytes(int num_pages) {
+    return fa::cache_collect_workspace_bytes(num_pages);
+}
+
+int fa_cache_collect(const int *block_table, const int *seq_lens, int num_seqs,
+                     int max_pages_per_seq, int num_pages, int page_size, int *free_pages,
+                     int *free_count, void *workspace, size_t workspace_bytes, void *stream) {
+    if (num_seqs < 0 || max_pages_per_seq <= 0 || num_pages <= 0) return FA_ERR_INVALID_ARG;
+    if (page_size != 16 || num_seqs > 65535 || (long long)num_pages * page_size > INT32_MAX / 2 ||
+        (long long)max_pages_per_seq * page_size > INT32_MAX / 2)
+        return FA_ERR_UNSUPPORTED;
+    if (!free_pages || !free_count || (num_seqs > 0 && (!block_table || !seq_lens)))
+        return FA_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(free_pages) ||
+        !aligned4(free_count))
+        return FA_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < fa::cache_collect_workspace_bytes(num_pages))
+        return FA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return FA_ERR_ALIGNMENT;
+    return map_rc(fa::launch_cache_collect(block_table, seq_lens, num_seqs, max_pages_per_seq,
+                                           num_pages, free_pages, free_count, workspace,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_cache_compact_workspace_bytes(int num_pages) {
+    return fa::cache_compact_workspace_bytes(num_pages);
+}
+
+int fa_cache_compact(void *k_cache, void *v_cache, float *k_scale, float *v_scale, int elem_bytes,
+                     const int *block_table, const int *seq_lens, int num_seqs,
+                     int *block_table_out, int *free_pages, int *free_count, int num_pages, int Hkv,
+                     int d, int page_size, int max_pages_per_seq, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    if (num_seqs < 0) return FA_ERR_INVALID_ARG;
+    const int rc = check_cache(k_cache, v_cache, k_scale, v_scale, elem_bytes, num_pages, Hkv, d,
+                               page_size, max_pages_per_seq);
+    if (rc) return rc;
+    if (num_seqs > 65535) return FA_ERR_UNSUPPORTED;
+    if (!free_pages || !free_count ||
+        (num_seqs > 0 && (!block_table || !seq_lens || !block_table_out)))
+        return FA_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(block_table_out) ||
+        !aligned4(free_pages) || !aligned4(free_count))
+        return FA_ERR_ALIGNMENT;
+    const size_t bytes = (size_t)num_seqs * max_pages_per_seq * 4;
+    if (block_table != block_table_out && overlap(block_table, bytes, block_table_out, bytes))
+        return FA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < fa::cache_compact_workspace_bytes(num_pages))
+        return FA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return FA_ERR_ALIGNMENT;
+    return map_rc(fa::launch_cache_compact(
+        cache_pages(k_cache, v_cache, k_scale, v_scale, elem_bytes, num_pages, Hkv, d), block_table,
+        seq_lens, num_seqs, max_pages_per_seq, block_table_out, free_pages, free_count, workspace,
+        static_cast<cudaStream_t>(stream)));
+}
+
 const char *fa_status_string(int status) {
     switch (status) {
     case FA_OK: return "ok";
@@ -611,6 +780,7 @@ const char *fa_status_string(int status) {
     case FA_ERR_WORKSPACE: return "workspace missing or too small";
     case FA_ERR_CUDA: return "CUDA runtime error";
     case FA_ERR_TIMEOUT: return "device-side wait timed out";
+    case FA_ERR_PAGES: return "no free cache page left";
     default: return "unknown status";
     }
 }
@@ -626,6 +796,7 @@ int fa_check_device_error(void *stream) {
         return FA_ERR_CUDA;
     if (word == fa::kDevErrTimeout) return FA_ERR_TIMEOUT;
     if (word == fa::kDevErrInput) return FA_ERR_INVALID_ARG;
+    if (word == fa::kDevErrPages) return FA_ERR_PAGES;
     return word ? FA_ERR_CUDA : FA_OK;
 }
 

@@ -94,6 +94,36 @@ struct BwdArgs {
 size_t bwd_workspace_bytes(long long total_tokens, int Hq, int d);
 int launch_bwd(const BwdArgs &a, cudaStream_t stream);
 
+// Device error word (see report_error): no free cache page was left.
+constexpr int kDevErrPages = 3;
+
+// A paged K/V cache the page operators work on (cache_pages.cu): elements of
+// elem_bytes (2: bf16, 1: E4M3 codes with k_scale, v_scale [num_pages][Hkv]).
+struct CachePages {
+    void *k, *v;
+    float *k_scale, *v_scale;   // device, or nullptr
+    int num_pages, Hkv, d, elem_bytes;
+};
+
+int launch_cache_fork(const CachePages &c, const int *table, const int *lens, int slots_in,
+                      const int *parents, int slots_out, const int *free_pages,
+                      const int *free_count, int *table_out, int *lens_out, int *count_out,
+                      int max_pages, cudaStream_t stream);
+int launch_cache_append(const CachePages &c, const void *k_new, const void *v_new, const int *cu,
+                        int num_seqs, int total, int *table, const int *lens,
+                        const int *free_pages, const int *free_count, int *lens_out,
+                        int *count_out, int max_pages, cudaStream_t stream);
+int launch_cache_copy(const CachePages &c, const int *src, const int *dst, int n,
+                      cudaStream_t stream);
+size_t cache_collect_workspace_bytes(int num_pages);
+int launch_cache_collect(const int *table, const int *lens, int num_seqs, int max_pages,
+                         int num_pages, int *free_pages, int *free_count, void *workspace,
+                         cudaStream_t stream);
+size_t cache_compact_workspace_bytes(int num_pages);
+int launch_cache_compact(const CachePages &c, const int *table, const int *lens, int num_seqs,
+                         int max_pages, int *table_out, int *free_pages, int *free_count,
+                         void *workspace, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 

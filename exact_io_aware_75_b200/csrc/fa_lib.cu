@@ -7,3 +7,4 @@
 #include "decode_noalloc.cu"
 #include "bwd_sm100.cu"
 #include "fp8_prep.cu"
+#include "cache_pages.cu"

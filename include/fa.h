@@ -58,7 +58,8 @@ enum fa_status {
     FA_ERR_ALIGNMENT = -3,    /* a pointer is not 16-byte aligned */
     FA_ERR_WORKSPACE = -4,    /* workspace missing or smaller than required */
     FA_ERR_CUDA = -5,         /* the CUDA runtime reported an error */
-    FA_ERR_TIMEOUT = -6       /* a device-side wait ran out (fa_check_device_error) */
+    FA_ERR_TIMEOUT = -6,      /* a device-side wait ran out (fa_check_device_error) */
+    FA_ERR_PAGES = -7         /* no free cache page was left (fa_check_device_error) */
 };
 
 enum fa_out_dtype { FA_OUT_BF16 = 0, FA_OUT_FP32 = 1 };
@@ -399,14 +400,113 @@ int fa_decode_paged_noalloc(const void *q, const void *k_cache, const void *v_ca
                             int d, int page_size, int max_pages_per_seq, float scale,
                             void *stream);
 
+/*
+ * The pages of the cache ("Paging and prefix sharing": the cache lives in
+ * fixed-size pages reached through block tables, and sequences with a common
+ * prefix name the same pages).  Five calls make, fill, free and move pages;
+ * all bookkeeping is on the device, so they can be recorded in a CUDA graph.
+ *
+ * Shared by the five:
+ *   k_cache, v_cache [num_pages, page_size, Hkv, d]: bf16 (elem_bytes = 2;
+ *               k_scale, v_scale NULL) or E4M3 codes (elem_bytes = 1; k_scale,
+ *               v_scale [num_pages, Hkv] fp32, moved with their pages), as in
+ *               fa_decode_paged and fa_decode_paged_fp8.  page_size 16, d 64 or
+ *               128; caches 16-byte aligned, everything else 4-byte.
+ *   block_table [slots, max_pages_per_seq] int32, seq_lens [slots] int32: slot
+ *               s uses the first ceil(seq_len / 16) entries of its row; others
+ *               are never read.  A slot of length 0 is empty.  A page is in
+ *               use if a used entry names it, and may be named by several.
+ *   free_pages  [num_pages] int32 and free_count [1] int32: pages not in use.
+ *               Pages are taken from the end: the r-th page that a call needs,
+ *               in slot order, is free_pages[free_count - 1 - r].
+ *   Device-side errors: a length, page or offset out of range is reported
+ *               through fa_check_device_error as FA_ERR_INVALID_ARG, and what
+ *               it belongs to is left out (never read or written out of
+ *               bounds); a slot for which no free page is left is reported as
+ *               FA_ERR_PAGES.  Outputs that this leaves unspecified are named
+ *               below.
+ *   Results do not depend on the order in which blocks run, and a call
+ *   repeated on the same inputs gives the same result.
+ *
+ * fa_cache_fork: the next batch of slots.  New slot i continues slot
+ * parents[i] (-1: an empty slot): full pages are shared; a partly filled last
+ * page stays with the first i that continues its parent, and every later one
+ * gets a free page with the tokens (and scales) copied, so that appending to
+ * one does not disturb the other.  A parent that no slot continues is gone:
+ * its pages are free again at the next fa_cache_collect.  Beam search passes
+ * the winning beams, sampling n answers to a prompt passes n equal parents.
+ *   parents [num_new] int32, device
+ *   block_table_out [num_new, max_pages_per_seq], seq_lens_out [num_new],
+ *   free_count_out [1]: written; must not overlap block_table, seq_lens,
+ *   free_count (FA_ERR_INVALID_ARG).  Entries past a row's used ones are left
+ *   as they were.  A slot without a free page, or with a parent out of range,
+ *   comes out empty.  At most 8192 slots (FA_ERR_UNSUPPORTED).
+ *
+ * fa_cache_append: new tokens behind the sequences' ends (bf16 caches).
+ *   k_new, v_new [total_new, Hkv, d] bf16, packed by cu_new [num_seqs + 1]
+ *   int32 (0 = cu_new[0] <= ... <= cu_new[num_seqs] = total_new); slot i gets
+ *   tokens cu_new[i] .. cu_new[i+1]-1 at positions seq_lens[i] and up.  Pages
+ *   it needs are taken from free_pages and written into its row of
+ *   block_table, behind its used entries.
+ *   seq_lens_out [num_seqs], free_count_out [1]: written; must not be
+ *   seq_lens, free_count (FA_ERR_INVALID_ARG).  A slot for which the free
+ *   pages do not suffice, or that would not fit its row, is left as it was
+ *   (its length copied); slots behind it that need no page go on.  A partly
+ *   filled last page must belong to its slot alone (fa_cache_fork sees to
+ *   that).  At most 8192 slots.
+ *
+ * fa_cache_collect: free_pages and free_count from the tables: every page
+ * not in use, in descending order, so that the lowest is handed out first.
+ * To free a sequence, set its length to 0 (or fork without it) and collect.
+ * Entries of free_pages past free_count are left as they were.
+ *   workspace: fa_cache_collect_workspace_bytes(num_pages), 256-byte aligned.
+ *
+ * fa_cache_compact: moves the n_live pages in use to page numbers 0 ..
+ * n_live-1, so that the cache's end can be given up: the i-th used page >=
+ * n_live goes to the i-th free page < n_live.  block_table_out (may be
+ * block_table itself; used entries written, others left as they were) names
+ * the pages by their new numbers; free_pages and free_count are as
+ * fa_cache_collect would give them afterwards.  Used pages that stay, and all
+ * pages >= n_live, keep their contents.
+ *   workspace: fa_cache_compact_workspace_bytes(num_pages), 256-byte aligned.
+ *
+ * fa_cache_copy_pages: page src[i] to page dst[i] for i < n (int32, device),
+ * whole pages with their scales.  Entries with src = dst = -1 are unused.  An
+ * entry whose destination is another entry's source, or a later entry's
+ * destination, is left out and reported as FA_ERR_INVALID_ARG.
+ */
+int fa_cache_fork(void *k_cache, void *v_cache, float *k_scale, float *v_scale, int elem_bytes,
+                  const int *block_table, const int *seq_lens, int num_slots, const int *parents,
+                  int num_new, const int *free_pages, const int *free_count, int *block_table_out,
+                  int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
+                  int page_size, int max_pages_per_seq, void *stream);
+int fa_cache_append(const void *k_new, const void *v_new, const int *cu_new, int num_seqs,
+                    int total_new, void *k_cache, void *v_cache, int *block_table,
+                    const int *seq_lens, const int *free_pages, const int *free_count,
+                    int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
+                    int page_size, int max_pages_per_seq, void *stream);
+int fa_cache_copy_pages(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                        int elem_bytes, const int *src, const int *dst, int n, int num_pages,
+                        int Hkv, int d, int page_size, void *stream);
+size_t fa_cache_collect_workspace_bytes(int num_pages);
+int fa_cache_collect(const int *block_table, const int *seq_lens, int num_seqs,
+                     int max_pages_per_seq, int num_pages, int page_size, int *free_pages,
+                     int *free_count, void *workspace, size_t workspace_bytes, void *stream);
+size_t fa_cache_compact_workspace_bytes(int num_pages);
+int fa_cache_compact(void *k_cache, void *v_cache, float *k_scale, float *v_scale, int elem_bytes,
+                     const int *block_table, const int *seq_lens, int num_seqs,
+                     int *block_table_out, int *free_pages, int *free_count, int num_pages, int Hkv,
+                     int d, int page_size, int max_pages_per_seq, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
 /* Human-readable text of a status code (static storage). */
 const char *fa_status_string(int status);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word that a
- * kernel sets when one of its bounded waits runs out or it meets an input it
- * cannot honour.  Returns FA_OK, FA_ERR_TIMEOUT, FA_ERR_INVALID_ARG or
- * FA_ERR_CUDA.
+ * kernel sets when one of its bounded waits runs out, it meets an input it
+ * cannot honour, or a cache call finds no free page.  Returns FA_OK,
+ * FA_ERR_TIMEOUT, FA_ERR_INVALID_ARG, FA_ERR_PAGES or FA_ERR_CUDA.
  */
 int fa_check_device_error(void *stream);
 
