@@ -110,9 +110,10 @@ def _load():
     lib.fa_decode_paged.restype = i
     lib.fa_decode_paged_noalloc.argtypes = [vp] * 7 + [i] * 7 + [f, vp]
     lib.fa_decode_paged_noalloc.restype = i
-    lib.fa_cache_fork.argtypes = [vp] * 4 + [i, vp, vp, i, vp, i] + [vp] * 5 + [i] * 5 + [vp]
+    lib.fa_cache_fork.argtypes = ([vp] * 4 + [i, vp, vp, i, vp, i, vp, vp, i] + [vp] * 3 + [i] * 5
+                                  + [vp])
     lib.fa_cache_fork.restype = i
-    lib.fa_cache_append.argtypes = [vp] * 3 + [i, i] + [vp] * 8 + [i] * 5 + [vp]
+    lib.fa_cache_append.argtypes = ([vp] * 3 + [i, i] + [vp] * 6 + [i, vp, vp] + [i] * 5 + [vp])
     lib.fa_cache_append.restype = i
     lib.fa_cache_copy_pages.argtypes = [vp] * 4 + [i, vp, vp] + [i] * 5 + [vp]
     lib.fa_cache_copy_pages.restype = i
@@ -596,7 +597,7 @@ def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, fre
     """The next batch of slots: slot i continues slot parents[i] (-1: empty), sharing full
     pages and copying a partly filled last page for all but the first that continue it.
     caches [P,16,Hkv,d] (bf16, or E4M3 with scales [P,Hkv]), block_table [S,maxp], seq_lens
-    [S], parents [N], free_pages [P], free_count [1] int32 -> writes block_table_out [N,maxp],
+    [S], parents [N], free_pages [F], free_count [1] int32 -> writes block_table_out [N,maxp],
     seq_lens_out [N], free_count_out [1], which must not overlap the inputs."""
     k_cache, v_cache, eb = _need_cache(k_cache, v_cache, k_scale, v_scale)
     P, ps, Hkv, d = k_cache.shape
@@ -605,7 +606,7 @@ def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, fre
     S, maxp = block_table.shape
     N = parents.shape[0]
     _need_ints((S,), "seq_lens", seq_lens)
-    _need_ints((P,), "free_pages", free_pages)
+    _need(free_pages, torch.int32, 1, "free_pages")
     _need_ints((1,), "free_count", free_count)
     _need_ints((N, maxp), "block_table_out", block_table_out)
     _need_ints((N,), "seq_lens_out", seq_lens_out)
@@ -616,8 +617,9 @@ def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, fre
                     seq_lens_out=seq_lens_out, free_count_out=free_count_out):
         _check(_lib.fa_cache_fork(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), eb,
                                   _ptr(block_table), _ptr(seq_lens), S, _ptr(parents), N,
-                                  _ptr(free_pages), _ptr(free_count), _ptr(block_table_out),
-                                  _ptr(seq_lens_out), _ptr(free_count_out), P, Hkv, d, ps, maxp,
+                                  _ptr(free_pages), _ptr(free_count), free_pages.shape[0],
+                                  _ptr(block_table_out), _ptr(seq_lens_out),
+                                  _ptr(free_count_out), P, Hkv, d, ps, maxp,
                                   _stream(stream)), "fa_cache_fork")
 
 
@@ -625,7 +627,7 @@ def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, 
                  free_count, seq_lens_out, free_count_out, stream=None):
     """New tokens behind the sequences' ends.  k_new, v_new [T,Hkv,d] bf16 packed by cu_new
     [S+1]; caches [P,16,Hkv,d] bf16; block_table [S,maxp] (gets the pages taken), seq_lens
-    [S], free_pages [P], free_count [1] int32 -> writes seq_lens_out [S], free_count_out [1],
+    [S], free_pages [F], free_count [1] int32 -> writes seq_lens_out [S], free_count_out [1],
     which must not be the inputs."""
     _need(k_new, torch.bfloat16, 3, "k_new")
     _need(v_new, torch.bfloat16, 3, "v_new")
@@ -639,7 +641,7 @@ def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, 
     S, maxp = block_table.shape
     _need_ints((S + 1,), "cu_new", cu_new)
     _need_ints((S,), "seq_lens", seq_lens)
-    _need_ints((P,), "free_pages", free_pages)
+    _need(free_pages, torch.int32, 1, "free_pages")
     _need_ints((1,), "free_count", free_count)
     _need_ints((S,), "seq_lens_out", seq_lens_out)
     _need_ints((1,), "free_count_out", free_count_out)
@@ -649,8 +651,8 @@ def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, 
                     free_count_out=free_count_out):
         _check(_lib.fa_cache_append(_ptr(k_new), _ptr(v_new), _ptr(cu_new), S, T, _ptr(k_cache),
                                     _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
-                                    _ptr(free_pages), _ptr(free_count), _ptr(seq_lens_out),
-                                    _ptr(free_count_out), P, Hkv, d, ps, maxp, _stream(stream)),
+                                    _ptr(free_pages), _ptr(free_count), free_pages.shape[0],
+                                    _ptr(seq_lens_out), _ptr(free_count_out), P, Hkv, d, ps, maxp, _stream(stream)),
                "fa_cache_append")
 
 

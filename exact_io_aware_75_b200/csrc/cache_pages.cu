@@ -114,9 +114,9 @@ __device__ __forceinline__ int good_len(int len, int max_pages) {
     return len;
 }
 
-__device__ __forceinline__ int good_count(const int *count, int num_pages) {
+__device__ __forceinline__ int good_count(const int *count, int capacity) {
     const int c = __ldg(count);
-    if (c < 0 || c > num_pages) {
+    if (c < 0 || c > capacity) {
         report_error(kDevErrInput);
         return 0;
     }
@@ -133,7 +133,7 @@ __device__ __forceinline__ int good_count(const int *count, int num_pages) {
 __global__ void __launch_bounds__(kThreads)
 fork_kernel(Pages pg, const int *__restrict__ table, const int *__restrict__ lens,
             const int *__restrict__ parents, const int *__restrict__ free_pages,
-            const int *__restrict__ free_count, int *__restrict__ table_out,
+            const int *__restrict__ free_count, int free_capacity, int *__restrict__ table_out,
             int *__restrict__ lens_out, int *__restrict__ count_out, int slots_in, int slots_out,
             int max_pages, int per_block) {
     extern __shared__ int s_first[];
@@ -163,7 +163,7 @@ fork_kernel(Pages pg, const int *__restrict__ table, const int *__restrict__ len
         if (i < e0) before += c;
     }
     int rank = block_sum(before, s_warp);
-    const int count = good_count(free_count, pg.num_pages);
+    const int count = good_count(free_count, free_capacity);
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         all = block_sum(all, s_warp);
         if (tid == 0) *count_out = count - min(all, count);
@@ -211,13 +211,13 @@ __global__ void __launch_bounds__(kThreads)
 append_kernel(Pages pg, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
               const int *__restrict__ cu, int *__restrict__ table, const int *__restrict__ lens,
               const int *__restrict__ free_pages, const int *__restrict__ free_count,
-              int *__restrict__ lens_out, int *__restrict__ count_out, int num_seqs, int total,
+              int free_capacity, int *__restrict__ lens_out, int *__restrict__ count_out, int num_seqs, int total,
               int max_pages, int per_block) {
     extern __shared__ int s_base[];
     __shared__ int s_warp[kWarps];
     __shared__ int s_row[kTokMax];
     const int tid = threadIdx.x;
-    const int count = good_count(free_count, pg.num_pages);
+    const int count = good_count(free_count, free_capacity);
     // what sequence s asks for; false: unusable offsets or lengths
     auto ask = [&](int s, int &len, int &n) -> bool {
         const int a = __ldg(cu + s);
@@ -516,29 +516,30 @@ using namespace cache_impl;
 
 int launch_cache_fork(const CachePages &c, const int *table, const int *lens, int slots_in,
                       const int *parents, int slots_out, const int *free_pages,
-                      const int *free_count, int *table_out, int *lens_out, int *count_out,
-                      int max_pages, cudaStream_t stream) {
+                      const int *free_count, int free_capacity, int *table_out, int *lens_out,
+                      int *count_out, int max_pages, cudaStream_t stream) {
     // a slot or a few per block, about four blocks per SM
     const int want = 2 * device_sm_count();
     const int per = slots_out > want ? (slots_out + want - 1) / want : 1;
     const int blocks = slots_out > 0 ? (slots_out + per - 1) / per : 1;
     fork_kernel<<<dim3(blocks, 2), kThreads, (size_t)slots_in * sizeof(int), stream>>>(
-        make_pages(c), table, lens, parents, free_pages, free_count, table_out, lens_out, count_out,
-        slots_in, slots_out, max_pages, per);
+        make_pages(c), table, lens, parents, free_pages, free_count, free_capacity, table_out, lens_out,
+        count_out, slots_in, slots_out, max_pages, per);
     return launched();
 }
 
 int launch_cache_append(const CachePages &c, const void *k_new, const void *v_new, const int *cu,
                         int num_seqs, int total, int *table, const int *lens,
-                        const int *free_pages, const int *free_count, int *lens_out,
-                        int *count_out, int max_pages, cudaStream_t stream) {
+                        const int *free_pages, const int *free_count, int free_capacity,
+                        int *lens_out, int *count_out, int max_pages, cudaStream_t stream) {
     const int want = 4 * device_sm_count();
     int per = (total + want - 1) / want;
     per = per < 1 ? 1 : per > kTokMax ? kTokMax : per;
     const int blocks = total > 0 ? (total + per - 1) / per : 1;
     append_kernel<<<blocks, kThreads, (size_t)num_seqs * sizeof(int), stream>>>(
         make_pages(c), static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new), cu,
-        table, lens, free_pages, free_count, lens_out, count_out, num_seqs, total, max_pages, per);
+        table, lens, free_pages, free_count, free_capacity, lens_out, count_out, num_seqs, total,
+        max_pages, per);
     return launched();
 }
 

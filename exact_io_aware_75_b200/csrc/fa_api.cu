@@ -647,10 +647,10 @@ extern "C" {
 
 int fa_cache_fork(void *k_cache, void *v_cache, float *k_scale, float *v_scale, int elem_bytes,
                   const int *block_table, const int *seq_lens, int num_slots, const int *parents,
-                  int num_new, const int *free_pages, const int *free_count, int *block_table_out,
-                  int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
+                  int num_new, const int *free_pages, const int *free_count, int free_capacity,
+                  int *block_table_out, int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
                   int page_size, int max_pages_per_seq, void *stream) {
-    if (num_slots < 0 || num_new < 0) return FA_ERR_INVALID_ARG;
+    if (num_slots < 0 || num_new < 0 || free_capacity < 0) return FA_ERR_INVALID_ARG;
     const int rc = check_cache(k_cache, v_cache, k_scale, v_scale, elem_bytes, num_pages, Hkv, d,
                                page_size, max_pages_per_seq);
     if (rc) return rc;
@@ -669,16 +669,17 @@ int fa_cache_fork(void *k_cache, void *v_cache, float *k_scale, float *v_scale, 
         return FA_ERR_INVALID_ARG;
     return map_rc(fa::launch_cache_fork(
         cache_pages(k_cache, v_cache, k_scale, v_scale, elem_bytes, num_pages, Hkv, d), block_table,
-        seq_lens, num_slots, parents, num_new, free_pages, free_count, block_table_out,
-        seq_lens_out, free_count_out, max_pages_per_seq, static_cast<cudaStream_t>(stream)));
+        seq_lens, num_slots, parents, num_new, free_pages, free_count, free_capacity,
+        block_table_out, seq_lens_out, free_count_out, max_pages_per_seq, static_cast<cudaStream_t>(stream)));
 }
 
 int fa_cache_append(const void *k_new, const void *v_new, const int *cu_new, int num_seqs,
                     int total_new, void *k_cache, void *v_cache, int *block_table,
                     const int *seq_lens, const int *free_pages, const int *free_count,
-                    int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
+                    int free_capacity, int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
                     int page_size, int max_pages_per_seq, void *stream) {
-    if (num_seqs < 0 || total_new < 0 || (num_seqs == 0 && total_new > 0)) return FA_ERR_INVALID_ARG;
+    if (num_seqs < 0 || total_new < 0 || (num_seqs == 0 && total_new > 0) || free_capacity < 0)
+        return FA_ERR_INVALID_ARG;
     const int rc = check_cache(k_cache, v_cache, nullptr, nullptr, 2, num_pages, Hkv, d, page_size,
                                max_pages_per_seq);
     if (rc) return rc;
@@ -696,7 +697,7 @@ int fa_cache_append(const void *k_new, const void *v_new, const int *cu_new, int
         return FA_ERR_INVALID_ARG;
     return map_rc(fa::launch_cache_append(
         cache_pages(k_cache, v_cache, nullptr, nullptr, 2, num_pages, Hkv, d), k_new, v_new, cu_new,
-        num_seqs, total_new, block_table, seq_lens, free_pages, free_count, seq_lens_out,
+        num_seqs, total_new, block_table, seq_lens, free_pages, free_count, free_capacity, seq_lens_out,
         free_count_out, max_pages_per_seq, static_cast<cudaStream_t>(stream)));
 }
 

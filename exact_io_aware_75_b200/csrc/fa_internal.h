@@ -107,12 +107,12 @@ struct CachePages {
 
 int launch_cache_fork(const CachePages &c, const int *table, const int *lens, int slots_in,
                       const int *parents, int slots_out, const int *free_pages,
-                      const int *free_count, int *table_out, int *lens_out, int *count_out,
-                      int max_pages, cudaStream_t stream);
+                      const int *free_count, int free_capacity, int *table_out, int *lens_out,
+                      int *count_out, int max_pages, cudaStream_t stream);
 int launch_cache_append(const CachePages &c, const void *k_new, const void *v_new, const int *cu,
                         int num_seqs, int total, int *table, const int *lens,
-                        const int *free_pages, const int *free_count, int *lens_out,
-                        int *count_out, int max_pages, cudaStream_t stream);
+                        const int *free_pages, const int *free_count, int free_capacity,
+                        int *lens_out, int *count_out, int max_pages, cudaStream_t stream);
 int launch_cache_copy(const CachePages &c, const int *src, const int *dst, int n,
                       cudaStream_t stream);
 size_t cache_collect_workspace_bytes(int num_pages);

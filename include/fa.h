@@ -416,7 +416,9 @@ int fa_decode_paged_noalloc(const void *q, const void *k_cache, const void *v_ca
  *               s uses the first ceil(seq_len / 16) entries of its row; others
  *               are never read.  A slot of length 0 is empty.  A page is in
  *               use if a used entry names it, and may be named by several.
- *   free_pages  [num_pages] int32 and free_count [1] int32: pages not in use.
+ *   free_pages  int32 and free_count [1] int32: pages not in use.  The calls
+ *               that take pages are given the length of free_pages
+ *               (free_capacity), the calls that write it need num_pages.
  *               Pages are taken from the end: the r-th page that a call needs,
  *               in slot order, is free_pages[free_count - 1 - r].
  *   Device-side errors: a length, page or offset out of range is reported
@@ -477,13 +479,13 @@ int fa_decode_paged_noalloc(const void *q, const void *k_cache, const void *v_ca
  */
 int fa_cache_fork(void *k_cache, void *v_cache, float *k_scale, float *v_scale, int elem_bytes,
                   const int *block_table, const int *seq_lens, int num_slots, const int *parents,
-                  int num_new, const int *free_pages, const int *free_count, int *block_table_out,
-                  int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
+                  int num_new, const int *free_pages, const int *free_count, int free_capacity,
+                  int *block_table_out, int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
                   int page_size, int max_pages_per_seq, void *stream);
 int fa_cache_append(const void *k_new, const void *v_new, const int *cu_new, int num_seqs,
                     int total_new, void *k_cache, void *v_cache, int *block_table,
                     const int *seq_lens, const int *free_pages, const int *free_count,
-                    int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
+                    int free_capacity, int *seq_lens_out, int *free_count_out, int num_pages, int Hkv, int d,
                     int page_size, int max_pages_per_seq, void *stream);
 int fa_cache_copy_pages(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
                         int elem_bytes, const int *src, const int *dst, int n, int num_pages,

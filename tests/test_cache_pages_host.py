@@ -15,14 +15,14 @@ def fa():
 
 
 def fork(fa, **kw):
-    a = dict(k=P, v=P, ks=0, vs=0, eb=2, bt=P, sl=P, S=4, par=P, N=4, fp=P, fc=P, bto=Q, slo=Q, fco=Q, np=100, Hkv=8,
+    a = dict(k=P, v=P, ks=0, vs=0, eb=2, bt=P, sl=P, S=4, par=P, N=4, fp=P, fc=P, cap=100, bto=Q, slo=Q, fco=Q, np=100, Hkv=8,
              d=128, ps=16, maxp=10)
     a.update(kw)
     return fa.library().fa_cache_fork(*a.values(), None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(S=-1), -1), (dict(N=-1), -1), (dict(k=0), -1), (dict(v=0), -1), (dict(eb=4), -1), (dict(eb=1), -1),
+    (dict(S=-1), -1), (dict(N=-1), -1), (dict(cap=-1), -1), (dict(k=0), -1), (dict(v=0), -1), (dict(eb=4), -1), (dict(eb=1), -1),
     (dict(ks=P, vs=P), -1), (dict(eb=1, ks=P), -1), (dict(np=0), -1), (dict(Hkv=0), -1), (dict(maxp=0), -1),
     (dict(d=96), -2), (dict(ps=32), -2), (dict(S=8193), -2), (dict(N=8193), -2), (dict(np=1 << 30), -2),
     (dict(bt=0), -1), (dict(sl=0), -1), (dict(par=0), -1), (dict(fp=0), -1), (dict(fc=0), -1), (dict(bto=0), -1),
@@ -34,14 +34,14 @@ def test_fork_rejects(fa, kw, status):
 
 
 def append(fa, **kw):
-    a = dict(kn=P, vn=P, cu=P, S=4, T=9, k=P, v=P, bt=P, sl=P, fp=P, fc=P, slo=Q, fco=Q, np=100, Hkv=8, d=128, ps=16,
+    a = dict(kn=P, vn=P, cu=P, S=4, T=9, k=P, v=P, bt=P, sl=P, fp=P, fc=P, cap=100, slo=Q, fco=Q, np=100, Hkv=8, d=128, ps=16,
              maxp=10)
     a.update(kw)
     return fa.library().fa_cache_append(*a.values(), None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(S=-1), -1), (dict(T=-1), -1), (dict(S=0), -1), (dict(kn=0), -1), (dict(cu=0), -1), (dict(k=0), -1),
+    (dict(S=-1), -1), (dict(T=-1), -1), (dict(cap=-2), -1), (dict(S=0), -1), (dict(kn=0), -1), (dict(cu=0), -1), (dict(k=0), -1),
     (dict(bt=0), -1), (dict(sl=0), -1), (dict(fp=0), -1), (dict(fc=0), -1), (dict(slo=0), -1), (dict(fco=0), -1),
     (dict(d=80), -2), (dict(ps=8), -2), (dict(S=9000), -2), (dict(T=(1 << 30) + 5), -2), (dict(vn=P + 8), -3),
     (dict(cu=P + 1), -3), (dict(slo=P), -1), (dict(fco=P), -1), (dict(np=0), -1)])
