@@ -14,6 +14,8 @@ Functions mirror the C entry points:
     decode_paged   -> fa_decode_paged   (paged split-KV decode)
     fp8_prepare    -> fa_fp8_prepare    (Hadamard rotation + E4M3 operands)
     fwd_fp8        -> fa_fwd_fp8        (FP8 prefill on those operands)
+    fwd_cross, fwd_varlen_cross, bwd_cross, bwd_varlen_cross
+                   -> fa_*_cross        (cross attention and its backward)
     cache_fork, cache_append, cache_copy_pages, cache_collect, cache_compact
                    -> fa_cache_*        (the pages of the cache)
     decode_paged_noalloc, decode_workspace_bytes, bwd_workspace_bytes,
@@ -48,6 +50,7 @@ EXPORTS = ("fa_fwd", "fa_fwd_varlen", "fa_fwd_sinks", "fa_fwd_varlen_sinks", "fa
            "fa_bwd_varlen_sinks",
            "fa_decode_workspace_bytes", "fa_decode_paged", "fa_decode_paged_sinks",
            "fa_decode_paged_fp8", "fa_fp8_workspace_bytes", "fa_fp8_prepare", "fa_fwd_fp8",
+           "fa_fwd_cross", "fa_fwd_varlen_cross", "fa_bwd_cross", "fa_bwd_varlen_cross",
            "fa_cache_fork", "fa_cache_append", "fa_cache_copy_pages",
            "fa_cache_collect_workspace_bytes", "fa_cache_collect",
            "fa_cache_compact_workspace_bytes", "fa_cache_compact",
@@ -110,6 +113,14 @@ def _load():
     lib.fa_decode_paged.restype = i
     lib.fa_decode_paged_noalloc.argtypes = [vp] * 7 + [i] * 7 + [f, vp]
     lib.fa_decode_paged_noalloc.restype = i
+    lib.fa_fwd_cross.argtypes = [vp] * 6 + [i] * 6 + [f, i, vp]
+    lib.fa_fwd_cross.restype = i
+    lib.fa_fwd_varlen_cross.argtypes = [vp] * 7 + [i] * 8 + [f, i, vp]
+    lib.fa_fwd_varlen_cross.restype = i
+    lib.fa_bwd_cross.argtypes = [vp] * 10 + [i] * 6 + [f, vp, sz, vp]
+    lib.fa_bwd_cross.restype = i
+    lib.fa_bwd_varlen_cross.argtypes = [vp] * 11 + [i] * 8 + [f, vp, sz, vp]
+    lib.fa_bwd_varlen_cross.restype = i
     lib.fa_cache_fork.argtypes = ([vp] * 4 + [i, vp, vp, i, vp, i, vp, vp, i] + [vp] * 3 + [i] * 5
                                   + [vp])
     lib.fa_cache_fork.restype = i
@@ -434,6 +445,143 @@ def bwd_varlen(q, k, v, o, dout, lse, cu_seqlens, max_seqlen, causal=False, wind
                               cu_seqlens.numel() - 1, T, int(max_seqlen), Hq, Hkv, d,
                               int(causal), int(window), float(scale), _ptr(workspace),
                               workspace.numel(), _stream(stream)), "fa_bwd_varlen")
+    return dq, dk, dv
+
+
+def _out_pair(out, lse, o_shape, lse_shape, out_dtype, return_lse, device):
+    """The output tensors of a forward call: given ones checked, missing ones made."""
+    if out is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise FAError(FA_ERR_INVALID_ARG, f"out_dtype {out_dtype}")
+        out = torch.empty(o_shape, dtype=out_dtype, device=device)
+    else:
+        _need(out, torch.float32 if out.dtype == torch.float32 else torch.bfloat16, len(o_shape), "out")
+        if tuple(out.shape) != tuple(o_shape):
+            raise FAError(FA_ERR_INVALID_ARG, "out shape")
+    if lse is not None:
+        _need(lse, torch.float32, len(lse_shape), "lse")
+        if tuple(lse.shape) != tuple(lse_shape):
+            raise FAError(FA_ERR_INVALID_ARG, "lse shape")
+    elif return_lse:
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
+    return out, lse, FA_OUT_FP32 if out.dtype == torch.float32 else FA_OUT_BF16
+
+
+def _same(t, ref, name):
+    """A tensor of ref's type and shape."""
+    _need(t, ref.dtype, ref.dim(), name)
+    if t.shape != ref.shape:
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} shape")
+    return t
+
+
+def _like(t, ref, name):
+    return torch.empty_like(ref) if t is None else _same(t, ref, name)
+
+
+def _cross_shapes(q, k, v, ndim):
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, torch.bfloat16, ndim, n)
+    if v.shape != k.shape or k.shape[-1] != q.shape[-1] or (ndim == 4 and k.shape[0] != q.shape[0]):
+        raise FAError(FA_ERR_INVALID_ARG, "q/k/v shape")
+
+
+def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, out=None, lse=None,
+              return_lse=True, stream=None):
+    """Cross attention, dense.  q [B,Nq,Hq,d], k/v [B,Nk,Hkv,d] bf16, seq_lens_k [B] int32
+    (device) or None -> (O [B,Nq,Hq,d], LSE [B,Hq,Nq])."""
+    _cross_shapes(q, k, v, 4)
+    B, Nq, Hq, d = q.shape
+    Nk, Hkv = k.shape[1:3]
+    if seq_lens_k is not None:
+        _need_ints((B,), "seq_lens_k", seq_lens_k)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out, lse, od = _out_pair(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), out_dtype, return_lse, q.device)
+    with _device_of(q, k=k, v=v, seq_lens_k=seq_lens_k, out=out, lse=lse):
+        _check(_lib.fa_fwd_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(seq_lens_k),
+                                 B, Hq, Hkv, Nq, Nk, d, float(scale), od, _stream(stream)),
+               "fa_fwd_cross")
+    return out, lse
+
+
+def fwd_varlen_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale=None,
+                     out_dtype=torch.bfloat16, out=None, lse=None, return_lse=True, stream=None):
+    """Cross attention, packed.  q [Tq,Hq,d], k/v [Tk,Hkv,d] bf16, cu_seqlens_q and
+    cu_seqlens_k [S+1] int32 (device) -> (O [Tq,Hq,d], LSE [Hq,Tq])."""
+    _cross_shapes(q, k, v, 3)
+    Tq, Hq, d = q.shape
+    Tk, Hkv = k.shape[:2]
+    _need(cu_seqlens_q, torch.int32, 1, "cu_seqlens_q")
+    _need_ints(cu_seqlens_q.shape, "cu_seqlens_k", cu_seqlens_k)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out, lse, od = _out_pair(out, lse, (Tq, Hq, d), (Hq, Tq), out_dtype, return_lse, q.device)
+    with _device_of(q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out,
+                    lse=lse):
+        _check(_lib.fa_fwd_varlen_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                        _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                                        cu_seqlens_q.numel() - 1, Tq, Tk, int(max_seqlen_q),
+                                        int(max_seqlen_k), Hq, Hkv, d, float(scale), od,
+                                        _stream(stream)), "fa_fwd_varlen_cross")
+    return out, lse
+
+
+def bwd_cross(q, k, v, o, dout, lse, seq_lens_k=None, scale=None, dq=None, dk=None, dv=None,
+              workspace=None, stream=None):
+    """Backward of fwd_cross.  q/o/dout [B,Nq,Hq,d], k/v [B,Nk,Hkv,d] bf16, lse [B,Hq,Nq]
+    -> (dQ, dK, dV) bf16."""
+    _cross_shapes(q, k, v, 4)
+    B, Nq, Hq, d = q.shape
+    Nk, Hkv = k.shape[1:3]
+    _same(o, q, "o")
+    _same(dout, q, "dout")
+    _need(lse, torch.float32, 3, "lse")
+    if tuple(lse.shape) != (B, Hq, Nq):
+        raise FAError(FA_ERR_INVALID_ARG, "lse shape")
+    if seq_lens_k is not None:
+        _need_ints((B,), "seq_lens_k", seq_lens_k)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dq, dk, dv = _like(dq, q, "dq"), _like(dk, k, "dk"), _like(dv, v, "dv")
+    workspace = _bytes_of(workspace, bwd_workspace_bytes(B * Nq, Hq, d), q.device)
+    with _device_of(q, k=k, v=v, o=o, dout=dout, lse=lse, seq_lens_k=seq_lens_k, dq=dq, dk=dk,
+                    dv=dv, workspace=workspace):
+        _check(_lib.fa_bwd_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
+                                 _ptr(dq), _ptr(dk), _ptr(dv), _ptr(seq_lens_k), B, Hq, Hkv, Nq,
+                                 Nk, d, float(scale), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)),
+               "fa_bwd_cross")
+    return dq, dk, dv
+
+
+def bwd_varlen_cross(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                     scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Backward of fwd_varlen_cross.  q/o/dout [Tq,Hq,d], k/v [Tk,Hkv,d] bf16, lse [Hq,Tq]
+    -> (dQ, dK, dV) bf16."""
+    _cross_shapes(q, k, v, 3)
+    Tq, Hq, d = q.shape
+    Tk, Hkv = k.shape[:2]
+    _same(o, q, "o")
+    _same(dout, q, "dout")
+    _need(lse, torch.float32, 2, "lse")
+    if tuple(lse.shape) != (Hq, Tq):
+        raise FAError(FA_ERR_INVALID_ARG, "lse shape")
+    _need(cu_seqlens_q, torch.int32, 1, "cu_seqlens_q")
+    _need_ints(cu_seqlens_q.shape, "cu_seqlens_k", cu_seqlens_k)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dq, dk, dv = _like(dq, q, "dq"), _like(dk, k, "dk"), _like(dv, v, "dv")
+    workspace = _bytes_of(workspace, bwd_workspace_bytes(Tq, Hq, d), q.device)
+    with _device_of(q, k=k, v=v, o=o, dout=dout, lse=lse, cu_seqlens_q=cu_seqlens_q,
+                    cu_seqlens_k=cu_seqlens_k, dq=dq, dk=dk, dv=dv, workspace=workspace):
+        _check(_lib.fa_bwd_varlen_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
+                                        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(cu_seqlens_q),
+                                        _ptr(cu_seqlens_k), cu_seqlens_q.numel() - 1, Tq, Tk,
+                                        int(max_seqlen_q), int(max_seqlen_k), Hq, Hkv, d,
+                                        float(scale), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(),
+                                        _stream(stream)), "fa_bwd_varlen_cross")
     return dq, dk, dv
 
 

@@ -104,6 +104,11 @@ struct Params {
     int causal, window;
     float scale, scale_log2;
     int num_kblocks, num_units;
+    // Cross attention: keys and values are tensors of their own, dense
+    // [num_seqs, seqlen_k] of which seq_lens_k[s] (if given) are visible, or
+    // packed by cu_seqlens_k.
+    const int *cu_seqlens_k, *seq_lens_k;
+    int seqlen_k, total_k, max_seqlen_k;
 };
 
 struct Unit {
@@ -111,14 +116,21 @@ struct Unit {
     int j0, jl;        // first and last key of the block (local to the sequence)
     int t_lo, nt;      // query tiles [t_lo, t_lo + nt) of each query head
     int ntiles;        // group * nt
+    int tokk0, Lk;     // first key and visible keys (tok0 and L but for cross attention)
+    int Ls;            // cross attention: stored keys; those past Lk get zero gradients
 };
 
+// False if the unit has no (query, key) pair.  Cross attention: w.Ls is then
+// the number of key rows that still get zero gradients.
+template <bool CROSS>
 __device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
     const int per = p.num_seqs * p.Hkv;
     const int jb = u / per;           // causal: low key blocks are the heaviest
     const int r = u % per;
     w.seq = r / p.Hkv;
     w.kvh = r % p.Hkv;
+    w.j0 = jb * kBlockK;
+    w.tokk0 = w.Ls = 0;
     if (p.cu_seqlens) {
         w.tok0 = __ldg(p.cu_seqlens + w.seq);
         w.L = __ldg(p.cu_seqlens + w.seq + 1) - w.tok0;
@@ -132,9 +144,30 @@ __device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
         w.tok0 = w.seq * p.seqlen;
         w.L = p.seqlen;
     }
-    w.j0 = jb * kBlockK;
-    if (w.L <= 0 || w.j0 >= w.L) return false;
-    w.jl = min(w.L, w.j0 + kBlockK) - 1;
+    if constexpr (CROSS) {
+        if (p.cu_seqlens_k) {
+            w.tokk0 = __ldg(p.cu_seqlens_k + w.seq);
+            w.Lk = __ldg(p.cu_seqlens_k + w.seq + 1) - w.tokk0;
+            if (w.tokk0 < 0 || w.Lk < 0 || w.Lk > p.max_seqlen_k || w.tokk0 > p.total_k - w.Lk) {
+                report_error(kDevErrInput);
+                return false;
+            }
+            w.Ls = w.Lk;
+        } else {
+            w.tokk0 = w.seq * p.seqlen_k;
+            w.Lk = p.seq_lens_k ? __ldg(p.seq_lens_k + w.seq) : p.seqlen_k;
+            if (w.Lk < 0 || w.Lk > p.seqlen_k) {
+                report_error(kDevErrInput);
+                return false;
+            }
+            w.Ls = p.seqlen_k;
+        }
+    } else {
+        w.tokk0 = w.tok0;
+        w.Lk = w.L;
+    }
+    if (w.L <= 0 || w.j0 >= w.Lk) return false;
+    w.jl = min(w.Lk, w.j0 + kBlockK) - 1;
     const int nq = (w.L + kBlockQ - 1) / kBlockQ;
     int lo = 0, hi = nq;
     if (p.causal) {
@@ -174,40 +207,66 @@ struct Shared {
     uint64_t ds_free[2];     // dK of the buffer's tile done: its dSᵀ buffer is free
     uint64_t acc_full, acc_free;
     uint64_t drain[2];
+    uint64_t kv_tail, qd_tail;   // cross attention: bytes of tiles with rows to clear
     uint32_t tmem_base;
     int abort;
 };
 
+// Cross attention: zeros over rows [valid, rows) of a tile of two 64-column
+// boxes, one warp.  What lies behind a sequence's end (other sequences,
+// padding, NaN included) would otherwise meet P = 0 or dS = 0 in a product.
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int rows, int valid, int box_bytes) {
+    const int n16 = (rows - valid) * 8;
+    for (int b = 0; b < kD / 64; ++b)
+        for (int i = lane_id(); i < n16; i += 32)
+            *reinterpret_cast<uint4 *>(tile + b * box_bytes + valid * 128 + i * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+}
+
 // ------------------------------------------------------------- TMA producer
+template <bool CROSS>
 __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const CUtensorMap *tmV,
                          const CUtensorMap *tmdO, const Params &p, Shared &sh, uint8_t *smem) {
     volatile int *abort = &sh.abort;
     const int lane = lane_id();
     float *rows = reinterpret_cast<float *>(smem + kOffRows);
-    uint32_t uc = 0, n = 0;
+    uint32_t uc = 0, n = 0, kv_tails = 0, qd_tails = 0;
     FOR_EACH_UNIT(u) {
         Unit w;
-        if (!get_unit(u, p, w)) continue;
+        if (!get_unit<CROSS>(u, p, w)) continue;
         if (!mbar_wait_warp(&sh.kv_empty, (uc & 1) ^ 1, abort)) goto out;
+        const bool kv_clear = CROSS && w.Lk - w.j0 < kBlockK && w.tokk0 + w.Lk < p.total_k;
+        uint64_t *kv_bar = kv_clear ? &sh.kv_tail : &sh.kv_full;
         if (lane == 0) {
-            mbar_arrive_expect_tx(&sh.kv_full, 2 * kKVTile);
+            mbar_arrive_expect_tx(kv_bar, 2 * kKVTile);
             for (int b = 0; b < kD / 64; ++b) {
-                tma_load_3d(smem + kOffK + b * kKVBox, tmK, &sh.kv_full, b * 64, w.kvh, w.tok0 + w.j0);
-                tma_load_3d(smem + kOffV + b * kKVBox, tmV, &sh.kv_full, b * 64, w.kvh, w.tok0 + w.j0);
+                tma_load_3d(smem + kOffK + b * kKVBox, tmK, kv_bar, b * 64, w.kvh, w.tokk0 + w.j0);
+                tma_load_3d(smem + kOffV + b * kKVBox, tmV, kv_bar, b * 64, w.kvh, w.tokk0 + w.j0);
             }
         }
         ++uc;
+        if (kv_clear) {
+            ++kv_tails;
+            if (!mbar_wait_warp(&sh.kv_tail, (kv_tails - 1) & 1, abort)) goto out;
+            clear_rows(smem + kOffK, kBlockK, w.Lk - w.j0, kKVBox);
+            clear_rows(smem + kOffV, kBlockK, w.Lk - w.j0, kKVBox);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.kv_full);
+        }
         for (int k = 0; k < w.ntiles; ++k, ++n) {
             const int s = n % kStages;
             if (!mbar_wait_warp(&sh.qd_empty[s], ((n / kStages) & 1) ^ 1, abort)) goto out;
             int h, q0;
             tile_of(w, p, k, h, q0);
+            uint8_t *st = smem + kOffStage + s * kStageBytes;
+            const bool qd_clear = CROSS && w.L - q0 < kBlockQ && w.tok0 + w.L < p.total_tokens;
+            uint64_t *qd_bar = qd_clear ? &sh.qd_tail : &sh.qd_full[s];
             if (lane == 0) {
-                uint8_t *st = smem + kOffStage + s * kStageBytes;
-                mbar_arrive_expect_tx(&sh.qd_full[s], 2 * kQTile);
+                mbar_arrive_expect_tx(qd_bar, 2 * kQTile);
                 for (int b = 0; b < kD / 64; ++b) {
-                    tma_load_3d(st + b * kQBox, tmQ, &sh.qd_full[s], b * 64, h, w.tok0 + q0);
-                    tma_load_3d(st + kQTile + b * kQBox, tmdO, &sh.qd_full[s], b * 64, h, w.tok0 + q0);
+                    tma_load_3d(st + b * kQBox, tmQ, qd_bar, b * 64, h, w.tok0 + q0);
+                    tma_load_3d(st + kQTile + b * kQBox, tmdO, qd_bar, b * 64, h, w.tok0 + q0);
                 }
             }
             // The tile's -LSE (log2 units) and -D; rows past the sequence get
@@ -225,13 +284,25 @@ __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const C
                 rs[rr] = -l2;
                 rs[kBlockQ + rr] = -dv;
             }
+            if (qd_clear) {
+                ++qd_tails;
+                if (!mbar_wait_warp(&sh.qd_tail, (qd_tails - 1) & 1, abort)) goto out;
+                clear_rows(st, kBlockQ, w.L - q0, kQBox);
+                clear_rows(st + kQTile, kBlockQ, w.L - q0, kQBox);
+                fence_proxy_async_smem();
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.qd_full[s]);
+            if (lane == 0) {
+                mbar_arrive(&sh.qd_full[s]);
+                if (qd_clear) mbar_arrive(&sh.qd_full[s]);   // in place of the byte count
+            }
         }
     }
     return;
 out:
     if (lane == 0) {
+        if (kv_tails) mbar_drain_wait(&sh.kv_tail, (kv_tails - 1) & 1);
+        if (qd_tails) mbar_drain_wait(&sh.qd_tail, (qd_tails - 1) & 1);
         if (uc) mbar_drain_wait(&sh.kv_full, (uc - 1) & 1);
         for (int s = 0; s < kStages; ++s)
             if (n > (uint32_t)s) mbar_drain_wait(&sh.qd_full[s], ((n - 1 - s) / kStages) & 1);
@@ -244,6 +315,7 @@ out:
 // of tile n overwrites the P^T that dV of tile n-2 reads, so it waits for
 // that MMA to complete; dP^T overwrites the dQ^T of tile n-2, so it waits
 // until that is drained.
+template <bool CROSS>
 __device__ void mma_issuer_s(const Params &p, Shared &sh, uint8_t *smem) {
     volatile int *abort = &sh.abort;
     const uint32_t tmem = sh.tmem_base;
@@ -254,7 +326,7 @@ __device__ void mma_issuer_s(const Params &p, Shared &sh, uint8_t *smem) {
     uint32_t uc = 0, n = 0;
     FOR_EACH_UNIT(u) {
         Unit w;
-        if (!get_unit(u, p, w)) continue;
+        if (!get_unit<CROSS>(u, p, w)) continue;
         if (!mbar_wait(&sh.kv_full, uc & 1, abort)) goto out;
         ++uc;
         for (int k = 0; k < w.ntiles; ++k, ++n) {
@@ -296,6 +368,7 @@ out:
 // per step, boxes of 64 columns LBO apart); dS^T sits in shared memory as 128
 // key rows of 64 queries, 128-byte swizzled: K-major A for dK, MN-major B
 // for dQ^T.
+template <bool CROSS>
 __device__ void mma_issuer_grad(const Params &p, Shared &sh, uint8_t *smem) {
     volatile int *abort = &sh.abort;
     const uint32_t tmem = sh.tmem_base;
@@ -306,7 +379,7 @@ __device__ void mma_issuer_grad(const Params &p, Shared &sh, uint8_t *smem) {
     uint32_t uc = 0, m = 0;
     FOR_EACH_UNIT(u) {
         Unit w;
-        if (!get_unit(u, p, w)) continue;
+        if (!get_unit<CROSS>(u, p, w)) continue;
         if (!mbar_wait(&sh.kv_full, uc & 1, abort)) goto out;
         ++uc;
         for (int k = 0; k < w.ntiles; ++k, ++m) {
@@ -416,7 +489,7 @@ __device__ __forceinline__ bool grad_row(uint32_t tS, uint32_t tdP, const float4
     return true;
 }
 
-template <int DH>
+template <int DH, bool CROSS>
 __device__ void softmax_wg(const Params &p, Shared &sh, uint8_t *smem) {
     volatile int *abort = &sh.abort;
     const int warp = warp_id(), lane = lane_id();
@@ -432,9 +505,18 @@ __device__ void softmax_wg(const Params &p, Shared &sh, uint8_t *smem) {
 
     FOR_EACH_UNIT(u) {
         Unit w;
-        if (!get_unit(u, p, w)) continue;
+        const bool any = get_unit<CROSS>(u, p, w);
         const int kj = w.j0 + r;                  // this thread's key
-        const bool key_ok = kj < w.L;
+        uint16_t *dst = static_cast<uint16_t *>(wg ? p.dk : p.dv) +
+                        ((size_t)(w.tokk0 + kj) * p.Hkv + w.kvh) * DH;
+        if (CROSS && kj < w.Ls && (!any || kj >= w.Lk)) {
+            // a key that no query sees
+            #pragma unroll
+            for (int c = 0; c < DH; c += 8)
+                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (!any) continue;
+        const bool key_ok = kj < w.Lk;
         for (int k = 0; k < w.ntiles; ++k, ++n) {
             if ((int)(n & 1) != wg) continue;
             const int s = n % kStages;
@@ -447,7 +529,7 @@ __device__ void softmax_wg(const Params &p, Shared &sh, uint8_t *smem) {
             const float4 *nl4 = reinterpret_cast<const float4 *>(rows + s * 2 * kBlockQ);
             const float4 *nd4 = nl4 + kBlockQ / 4;
             const int qmax = min(q0 + kBlockQ, w.L) - 1;
-            const bool edge = (w.j0 + kBlockK > w.L) || (p.causal && w.jl > q0) ||
+            const bool edge = (w.j0 + kBlockK > w.Lk) || (p.causal && w.jl > q0) ||
                               (p.window > 0 && w.j0 <= qmax - p.window);
             // The mask of an edge tile: the column range [lo_c, hi_c) of this
             // key's visible queries.
@@ -478,8 +560,6 @@ __device__ void softmax_wg(const Params &p, Shared &sh, uint8_t *smem) {
         tc_fence_after();
         const uint32_t tAcc = sh.tmem_base + lanes + (wg ? kColDK : kColDV);
         const float mul = wg ? p.scale : 1.f;
-        uint16_t *dst = static_cast<uint16_t *>(wg ? p.dk : p.dv) +
-                        ((size_t)(w.tok0 + kj) * p.Hkv + w.kvh) * DH;
         #pragma unroll
         for (int c = 0; c < kD; c += 32) {
             uint32_t v[32];
@@ -511,7 +591,7 @@ __device__ void softmax_wg(const Params &p, Shared &sh, uint8_t *smem) {
 // rows; two staging buffers alternate so the next rows are written while the
 // previous reduce still reads.  Rows past the sequence add exact zeros (their
 // P, hence dS, is 0).
-template <int DH>
+template <int DH, bool CROSS>
 __device__ void dq_drain(const CUtensorMap *tmDQ, const Params &p, Shared &sh, uint8_t *smem) {
     volatile int *abort = &sh.abort;
     const int warp = warp_id(), lane = lane_id();
@@ -522,7 +602,7 @@ __device__ void dq_drain(const CUtensorMap *tmDQ, const Params &p, Shared &sh, u
     uint32_t n = 0, hs = 0;
     FOR_EACH_UNIT(u) {
         Unit w;
-        if (!get_unit(u, p, w)) continue;
+        if (!get_unit<CROSS>(u, p, w)) continue;
         for (int k = 0; k < w.ntiles; ++k, ++n) {
             const int b = n & 1;
             const bool ok = mbar_wait_warp(&sh.dq_full[b], (n >> 1) & 1, abort);
@@ -561,7 +641,7 @@ out:
     if (leader) bulk_wait_group_all();
 }
 
-template <int DH>
+template <int DH, bool CROSS>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -591,6 +671,8 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         mbar_init(&sh.acc_free, 8);
         mbar_init(&sh.drain[0], 1);
         mbar_init(&sh.drain[1], 1);
+        mbar_init(&sh.kv_tail, 1);
+        mbar_init(&sh.qd_tail, 1);
         sh.abort = 0;
         fence_barrier_init();
     }
@@ -608,18 +690,18 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 
     if (warp < 8) {
         regs_increase<kRegsSoftmax>();
-        softmax_wg<DH>(p, sh, smem);
+        softmax_wg<DH, CROSS>(p, sh, smem);
     } else if (warp < 12) {
         regs_decrease<kRegsDrain>();
-        dq_drain<DH>(&tmDQ, p, sh, smem);
+        dq_drain<DH, CROSS>(&tmDQ, p, sh, smem);
     } else {
         regs_decrease<kRegsControl>();
         if (warp == kWarpTma) {
-            producer(&tmQ, &tmK, &tmV, &tmdO, p, sh, smem);
+            producer<CROSS>(&tmQ, &tmK, &tmV, &tmdO, p, sh, smem);
         } else if (warp == kWarpMma) {
-            if (lane_id() == 0) mma_issuer_s(p, sh, smem);
+            if (lane_id() == 0) mma_issuer_s<CROSS>(p, sh, smem);
         } else if (warp == kWarpMmaGrad) {
-            if (lane_id() == 0) mma_issuer_grad(p, sh, smem);
+            if (lane_id() == 0) mma_issuer_grad<CROSS>(p, sh, smem);
         }
     }
     __syncwarp();
@@ -705,11 +787,18 @@ bwd_dsink_kernel(const float *__restrict__ lse, const float *__restrict__ dd,
     }
 }
 
-// dQ (bf16) = the fp32 accumulator, eight elements per thread.
+// dQ (bf16) = the fp32 accumulator, eight elements per thread.  With cu (cross
+// attention, packed) only rows of the sequences, cu[0] .. cu[num_seqs]-1;
+// per8: threads per token.
 __global__ void __launch_bounds__(256)
-bwd_convert_kernel(const float *__restrict__ acc, uint16_t *__restrict__ dq, long long n8) {
+bwd_convert_kernel(const float *__restrict__ acc, uint16_t *__restrict__ dq, long long n8,
+                   const int *__restrict__ cu, int num_seqs, int per8) {
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n8) return;
+    if (cu) {
+        const long long t = i / per8;
+        if (t < __ldg(cu) || t >= __ldg(cu + num_seqs)) return;
+    }
     const float4 a = reinterpret_cast<const float4 *>(acc)[2 * i];
     const float4 b = reinterpret_cast<const float4 *>(acc)[2 * i + 1];
     uint4 o;
@@ -718,6 +807,18 @@ bwd_convert_kernel(const float *__restrict__ acc, uint16_t *__restrict__ dq, lon
     o.z = pack_bf16(b.x, b.y);
     o.w = pack_bf16(b.z, b.w);
     reinterpret_cast<uint4 *>(dq)[i] = o;
+}
+
+// Zeros into rows cu[0] .. cu[num_seqs]-1 of two tensors (all rows without
+// cu); n8 16-byte words, per8 per row.  Cross attention without any query.
+__global__ void __launch_bounds__(256)
+bwd_zero_kernel(uint4 *__restrict__ dk, uint4 *__restrict__ dv, long long n8,
+                const int *__restrict__ cu, int num_seqs, int per8) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n8) return;
+    if (cu && (i / per8 < __ldg(cu) || i / per8 >= __ldg(cu + num_seqs))) return;
+    dk[i] = make_uint4(0u, 0u, 0u, 0u);
+    dv[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 }  // namespace bwd_impl
@@ -734,7 +835,16 @@ int launch_bwd(const BwdArgs &a, cudaStream_t stream) {
     if (a.d != 64 && a.d != 128) return -2;
     const int dh = a.d;
     const long long total = a.total_tokens;
-    if (total == 0 || a.num_seqs == 0) return 0;
+    if (a.num_seqs == 0) return 0;
+    if (total == 0) {
+        if (!a.cross || a.total_k == 0) return 0;
+        const int per8 = a.Hkv * dh / 8;
+        const long long n8 = (long long)a.total_k * per8;
+        bwd_zero_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, stream>>>(
+            static_cast<uint4 *>(a.dk), static_cast<uint4 *>(a.dv), n8, a.cu_seqlens_k, a.num_seqs,
+            per8);
+        return cudaGetLastError() == cudaSuccess ? 0 : -5;
+    }
     const size_t acc_bytes = ((size_t)total * a.Hq * dh * sizeof(float) + 255) & ~(size_t)255;
     float *dq_acc = static_cast<float *>(a.workspace);
     float *dd = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + acc_bytes);
@@ -758,13 +868,17 @@ int launch_bwd(const BwdArgs &a, cudaStream_t stream) {
     // S or dP, and their dK, dV, dQ columns are never written.
     alignas(64) CUtensorMap tq, tk, tv, tdo, tdq;
     const uint64_t T = (uint64_t)total;
+    // (without any key the K and V maps are never used: any valid address)
+    const bool no_keys = a.cross && a.total_k == 0;
+    const uint64_t TK = no_keys ? 1 : a.cross ? (uint64_t)a.total_k : T;
+    const void *k = no_keys ? a.q : a.k, *v = no_keys ? a.q : a.v;
     if (encode_tensor_map_3d(&tq, a.q, 2, dh, a.Hq, T, (uint64_t)dh * 2, (uint64_t)a.Hq * dh * 2,
                              64, 1, kBlockQ, 128) ||
         encode_tensor_map_3d(&tdo, a.dout, 2, dh, a.Hq, T, (uint64_t)dh * 2,
                              (uint64_t)a.Hq * dh * 2, 64, 1, kBlockQ, 128) ||
-        encode_tensor_map_3d(&tk, a.k, 2, dh, a.Hkv, T, (uint64_t)dh * 2,
+        encode_tensor_map_3d(&tk, k, 2, dh, a.Hkv, TK, (uint64_t)dh * 2,
                              (uint64_t)a.Hkv * dh * 2, 64, 1, kBlockK, 128) ||
-        encode_tensor_map_3d(&tv, a.v, 2, dh, a.Hkv, T, (uint64_t)dh * 2,
+        encode_tensor_map_3d(&tv, v, 2, dh, a.Hkv, TK, (uint64_t)dh * 2,
                              (uint64_t)a.Hkv * dh * 2, 64, 1, kBlockK, 128) ||
         encode_tensor_map_3d(&tdq, dq_acc, 4, dh, a.Hq, T, (uint64_t)dh * 4,
                              (uint64_t)a.Hq * dh * 4, dh, 1, kDQHalf, 0))
@@ -787,12 +901,18 @@ int launch_bwd(const BwdArgs &a, cudaStream_t stream) {
     p.window = a.causal ? a.window : 0;
     p.scale = a.scale;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    p.num_kblocks = (a.max_seqlen + kBlockK - 1) / kBlockK;
+    p.cu_seqlens_k = a.cu_seqlens_k;
+    p.seq_lens_k = a.seq_lens_k;
+    p.seqlen_k = a.seqlen_k;
+    p.total_k = a.total_k;
+    p.max_seqlen_k = a.max_seqlen_k;
+    p.num_kblocks = ((a.cross ? a.max_seqlen_k : a.max_seqlen) + kBlockK - 1) / kBlockK;
     const long long units = (long long)p.num_kblocks * a.num_seqs * a.Hkv;
     if (units > (1ll << 30)) return -2;
     p.num_units = (int)units;
     if (units > 0) {
-        auto kernel = dh == 128 ? bwd_kernel<128> : bwd_kernel<64>;
+        auto kernel = a.cross ? (dh == 128 ? bwd_kernel<128, true> : bwd_kernel<64, true>)
+                              : (dh == 128 ? bwd_kernel<128, false> : bwd_kernel<64, false>);
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmemBytes) != cudaSuccess)
             return -5;
@@ -802,7 +922,8 @@ int launch_bwd(const BwdArgs &a, cudaStream_t stream) {
     }
     const long long n8 = total * a.Hq * dh / 8;
     bwd_convert_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, stream>>>(
-        dq_acc, static_cast<uint16_t *>(a.dq), n8);
+        dq_acc, static_cast<uint16_t *>(a.dq), n8, a.cross ? a.cu_seqlens : nullptr, a.num_seqs,
+        a.Hq * dh / 8);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 

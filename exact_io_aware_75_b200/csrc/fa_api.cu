@@ -772,6 +772,138 @@ int fa_cache_compact(void *k_cache, void *v_cache, float *k_scale, float *v_scal
         static_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// Pointers and sizes that the cross-attention calls share.
+int check_cross(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                const int *seq_lens_k, const int *cu_q, const int *cu_k, bool packed,
+                long long total_q, long long total_k) {
+    if (packed && (!cu_q || !cu_k)) return FA_ERR_INVALID_ARG;
+    if (total_q > 0 && (!q || !o)) return FA_ERR_INVALID_ARG;
+    if (total_k > 0 && (!k || !v)) return FA_ERR_INVALID_ARG;
+    if (total_q > INT32_MAX / 2 || total_k > INT32_MAX / 2) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse) ||
+        !aligned4(seq_lens_k) || !aligned4(cu_q) || !aligned4(cu_k))
+        return FA_ERR_ALIGNMENT;
+    return FA_OK;
+}
+
+// Dense (cu_q = cu_k = NULL: num_seqs sequences of Nq queries and Nk keys) or packed.
+int fwd_cross_call(const void *q, const void *k, const void *v, void *o, float *lse,
+                   const int *seq_lens_k, const int *cu_q, const int *cu_k, bool packed,
+                   int num_seqs, long long total_q, long long total_k, int max_q, int max_k, int Hq,
+                   int Hkv, int d, float scale, int o_dtype, void *stream) {
+    if (num_seqs < 0 || total_q < 0 || total_k < 0 || max_q < 0 || max_k < 0)
+        return FA_ERR_INVALID_ARG;
+    int rc = check_common(Hq, Hkv, d, 0, 0, scale, o_dtype);
+    if (rc) return rc;
+    if (num_seqs == 0 || total_q == 0 || max_q == 0) return FA_OK;
+    rc = check_cross(q, k, v, o, lse, seq_lens_k, cu_q, cu_k, packed, total_q, total_k);
+    if (rc) return rc;
+    fa::PrefillArgs a{};
+    a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
+    a.cu_seqlens = cu_q;
+    a.num_seqs = num_seqs;
+    a.seqlen = packed ? 0 : max_q;
+    a.total_tokens = (int)total_q;
+    a.max_seqlen = max_q;
+    a.Hq = Hq; a.Hkv = Hkv; a.d = d;
+    a.scale = scale;
+    a.o_fp32 = o_dtype == FA_OUT_FP32;
+    a.cross = 1;
+    a.cu_seqlens_k = cu_k;
+    a.seq_lens_k = seq_lens_k;
+    a.seqlen_k = packed ? 0 : max_k;
+    a.total_k = (int)total_k;
+    a.max_seqlen_k = max_k;
+    return map_rc(fa::launch_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+int bwd_cross_call(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                   const float *lse, void *dq, void *dk, void *dv, const int *seq_lens_k,
+                   const int *cu_q, const int *cu_k, bool packed, int num_seqs, long long total_q,
+                   long long total_k, int max_q, int max_k, int Hq, int Hkv, int d, float scale,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+    if (num_seqs < 0 || total_q < 0 || total_k < 0 || max_q < 0 || max_k < 0)
+        return FA_ERR_INVALID_ARG;
+    int rc = check_common(Hq, Hkv, d, 0, 0, scale, FA_OUT_BF16);
+    if (rc) return rc;
+    if (num_seqs == 0 || (total_q == 0 && total_k == 0)) return FA_OK;
+    rc = check_cross(q, k, v, o, lse, seq_lens_k, cu_q, cu_k, packed, total_q, total_k);
+    if (rc) return rc;
+    if (total_q > 0 && (!dout || !lse || !dq)) return FA_ERR_INVALID_ARG;
+    if (total_k > 0 && (!dk || !dv)) return FA_ERR_INVALID_ARG;
+    if (total_q * Hq > INT32_MAX / 2) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+        return FA_ERR_ALIGNMENT;
+    if (total_q > 0) {
+        if (!workspace || workspace_bytes < fa::bwd_workspace_bytes(total_q, Hq, d))
+            return FA_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(workspace) & 255) return FA_ERR_ALIGNMENT;
+    }
+    fa::BwdArgs a{};
+    a.q = q; a.k = k; a.v = v; a.o = o; a.dout = dout; a.lse = lse;
+    a.dq = dq; a.dk = dk; a.dv = dv;
+    a.cu_seqlens = cu_q;
+    a.num_seqs = num_seqs;
+    a.seqlen = packed ? 0 : max_q;
+    a.total_tokens = (int)total_q;
+    a.max_seqlen = max_q;
+    a.Hq = Hq; a.Hkv = Hkv; a.d = d;
+    a.scale = scale;
+    a.workspace = workspace;
+    a.cross = 1;
+    a.cu_seqlens_k = cu_k;
+    a.seq_lens_k = seq_lens_k;
+    a.seqlen_k = packed ? 0 : max_k;
+    a.total_k = (int)total_k;
+    a.max_seqlen_k = max_k;
+    return map_rc(fa::launch_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_fwd_cross(const void *q, const void *k, const void *v, void *o, float *lse,
+                 const int *seq_lens_k, int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale,
+                 int o_dtype, void *stream) {
+    if (B < 0 || Nq < 0 || Nk < 0) return FA_ERR_INVALID_ARG;
+    return fwd_cross_call(q, k, v, o, lse, seq_lens_k, nullptr, nullptr, false, B, (long long)B * Nq,
+                          (long long)B * Nk, Nq, Nk, Hq, Hkv, d, scale, o_dtype, stream);
+}
+
+int fa_fwd_varlen_cross(const void *q, const void *k, const void *v, void *o, float *lse,
+                        const int *cu_seqlens_q, const int *cu_seqlens_k, int num_seqs, int total_q,
+                        int total_k, int max_seqlen_q, int max_seqlen_k, int Hq, int Hkv, int d,
+                        float scale, int o_dtype, void *stream) {
+    return fwd_cross_call(q, k, v, o, lse, nullptr, cu_seqlens_q, cu_seqlens_k, true, num_seqs,
+                          total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hkv, d, scale, o_dtype,
+                          stream);
+}
+
+int fa_bwd_cross(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                 const float *lse, void *dq, void *dk, void *dv, const int *seq_lens_k, int B, int Hq,
+                 int Hkv, int Nq, int Nk, int d, float scale, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+    if (B < 0 || Nq < 0 || Nk < 0) return FA_ERR_INVALID_ARG;
+    return bwd_cross_call(q, k, v, o, dout, lse, dq, dk, dv, seq_lens_k, nullptr, nullptr, false, B,
+                          (long long)B * Nq, (long long)B * Nk, Nq, Nk, Hq, Hkv, d, scale, workspace,
+                          workspace_bytes, stream);
+}
+
+int fa_bwd_varlen_cross(const void *q, const void *k, const void *v, const void *o,
+                        const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                        const int *cu_seqlens_q, const int *cu_seqlens_k, int num_seqs, int total_q,
+                        int total_k, int max_seqlen_q, int max_seqlen_k, int Hq, int Hkv, int d,
+                        float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    return bwd_cross_call(q, k, v, o, dout, lse, dq, dk, dv, nullptr, cu_seqlens_q, cu_seqlens_k,
+                          true, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hkv, d,
+                          scale, workspace, workspace_bytes, stream);
+}
+
 const char *fa_status_string(int status) {
     switch (status) {
     case FA_OK: return "ok";

@@ -30,6 +30,11 @@ struct PrefillArgs {
     const int *doc;
     // sink tokens kept visible beside a causal window (0 = none)
     int n_sink;
+    // cross attention: keys of their own, dense [num_seqs, seqlen_k] with
+    // seq_lens_k (or nullptr) visible ones, or packed by cu_seqlens_k
+    int cross;
+    const int *cu_seqlens_k;
+    int seqlen_k, total_k, max_seqlen_k;
     // FP8 operands (launch_prefill_fp8): q, k hold E4M3 codes, v the
     // transposed V codes [B, Hkv, d, vt_stride]; scales per (sequence, head,
     // 128-token block) for Q and K, per (sequence, KV head) for V
@@ -89,6 +94,10 @@ struct BwdArgs {
     void *workspace;
     const float *sinks;     // [Hq] learned sink logits, or nullptr
     float *dsinks;          // [Hq] their gradient (written when sinks is set)
+    // cross attention, as in PrefillArgs
+    int cross;
+    const int *cu_seqlens_k, *seq_lens_k;
+    int seqlen_k, total_k, max_seqlen_k;
 };
 
 size_t bwd_workspace_bytes(long long total_tokens, int Hq, int d);

@@ -117,6 +117,11 @@ struct Params {
     // Sink tokens (with causal and a window): keys j < n_sink of a sequence
     // stay visible to every later query; 0 = none.
     int n_sink;
+    // Cross attention: keys and values are tensors of their own.  Dense:
+    // seqlen_k stored keys per sequence, of which seq_lens_k[s] (if given) are
+    // visible; packed: cu_seqlens_k.
+    const int *cu_seqlens_k;
+    int seqlen_k, total_k, max_seqlen_k;
 };
 
 struct Unit {
@@ -126,6 +131,7 @@ struct Unit {
     int q0;     // first query row of the unit, local to the sequence
     int Lk;     // keys of the sequence (= L except for the paged chunked prefill)
     int off;    // key position of query row 0 (Lk - L)
+    int tokk0;  // cross attention: index of the sequence's first key
     int lo[2], hi[2];  // key-block range per tile, [lo, hi)
     int lo_all, hi_all;
     // Sink tokens: tile t also takes key blocks [0, ns[t]) (ns[t] <= lo[t]);
@@ -134,7 +140,7 @@ struct Unit {
     int ns[2], A;
 };
 
-template <bool PAGED, bool SINK = false>
+template <bool PAGED, bool SINK = false, bool CROSS = false>
 __device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
     int mb;
     if (PAGED) {
@@ -187,6 +193,27 @@ __device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
         w.Lk = Lk;
         w.off = Lk - w.L;
     }
+    if constexpr (CROSS) {
+        int Lk = p.seqlen_k;
+        if (p.cu_seqlens_k) {
+            w.tokk0 = __ldg(p.cu_seqlens_k + w.seq);
+            Lk = __ldg(p.cu_seqlens_k + w.seq + 1) - w.tokk0;
+            if (w.tokk0 < 0 || Lk < 0 || Lk > p.max_seqlen_k || w.tokk0 > p.total_k - Lk) {
+                report_error(kDevErrInput);
+                return false;
+            }
+        } else {
+            w.tokk0 = w.seq * p.seqlen_k;
+            if (p.seq_lens_k) {
+                Lk = __ldg(p.seq_lens_k + w.seq);
+                if (Lk < 0 || Lk > p.seqlen_k) {
+                    report_error(kDevErrInput);
+                    return false;
+                }
+            }
+        }
+        w.Lk = Lk;
+    }
     const int nkb = (w.Lk + kBlockN - 1) / kBlockN;
     w.lo_all = 1 << 30;
     w.hi_all = 0;
@@ -237,6 +264,7 @@ struct Shared {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full[2], p_lo[2], p_hi[2], o_full[2], o_empty[2];
     uint64_t drain;
+    uint64_t v_tail;      // cross attention: bytes of a V tile with rows to clear
     uint32_t tmem_base;
     int abort;
 };
@@ -405,8 +433,86 @@ out:
     }
 }
 
+// Cross attention: one warp.  As the dense producer, with keys at their own
+// offsets.  A tile in which the sequence's keys end may hold the next
+// sequence's rows or padding behind them, NaN included.  K's are masked as
+// scores; a V row there would be multiplied by P = 0, so it is cleared: that
+// V tile's bytes are counted on a barrier of their own, the warp waits for
+// them, writes zeros over the rows and only then completes the slot.
+template <int D>
+__device__ void producer_cross(const CUtensorMap *tmQ, const CUtensorMap *tmK,
+                               const CUtensorMap *tmV, const Params &p, Shared &sh, uint8_t *sQ,
+                               uint8_t *sKV) {
+    using C = Cfg<D>;
+    volatile int *abort = &sh.abort;
+    const int lane = lane_id();
+    uint32_t q_uses[2] = {0, 0};
+    uint32_t kv_it = 0, tails = 0;
+    FOR_EACH_UNIT(u) {
+        Unit w;
+        if (!get_unit<false, false, true>(u, p, w)) continue;
+        for (int t = 0; t < 2; ++t) {
+            if (w.lo[t] >= w.hi[t]) continue;
+            if (!mbar_wait_warp(&sh.q_empty[t], (q_uses[t] & 1) ^ 1, abort)) goto out;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh.q_full[t], C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sQ + t * C::kTileBytes + b * C::kBoxBytes, tmQ, &sh.q_full[t],
+                                b * C::kBoxCols, w.h, w.tok0 + w.q0 + t * kBlockM);
+            }
+            ++q_uses[t];
+        }
+        for (int j = w.lo_all; j < w.hi_all; ++j) {
+            const int valid = w.Lk - j * kBlockN;     // keys of the sequence in this tile
+            // rows past the tensor arrive as zeros by themselves
+            const bool clear = valid < kBlockN && w.tokk0 + w.Lk < p.total_k;
+            for (int kv = 0; kv < 2; ++kv) {
+                const int slot = kv_it % C::kStages;
+                uint8_t *dst = sKV + slot * C::kTileBytes;
+                const bool tail = kv == 1 && clear;
+                if (!mbar_wait_warp(&sh.kv_empty[slot], ((kv_it / C::kStages) & 1) ^ 1, abort))
+                    goto out;
+                uint64_t *bar = tail ? &sh.v_tail : &sh.kv_full[slot];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, C::kTileBytes);
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        tma_load_3d(dst + b * C::kBoxBytes, kv ? tmV : tmK, bar, b * C::kBoxCols,
+                                    w.kvh, w.tokk0 + j * kBlockN);
+                }
+                if (tail) {
+                    ++tails;
+                    if (!mbar_wait_warp(&sh.v_tail, (tails - 1) & 1, abort)) goto out;
+                    const int n16 = (kBlockN - valid) * 8;       // 16-byte words per box
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        for (int i = lane; i < n16; i += 32)
+                            *reinterpret_cast<uint4 *>(dst + b * C::kBoxBytes + valid * 128 + i * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
+                }
+                ++kv_it;
+            }
+        }
+    }
+    return;
+out:
+    // Leave no copy in flight: wait for the last load issued into each slot.
+    if (lane == 0) {
+        if (tails) mbar_drain_wait(&sh.v_tail, (tails - 1) & 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            if (kv_it > (uint32_t)s) {
+                const uint32_t last = (kv_it - 1 - s) / C::kStages;
+                mbar_drain_wait(&sh.kv_full[s], last & 1);
+            }
+        }
+        for (int t = 0; t < 2; ++t)
+            if (q_uses[t]) mbar_drain_wait(&sh.q_full[t], (q_uses[t] - 1) & 1);
+    }
+}
+
 // ------------------------------------------------------------ MMA issuer
-template <int D, bool PAGED, bool DOC, bool F8, bool SINK>
+template <int D, bool PAGED, bool DOC, bool F8, bool SINK, bool CROSS>
 __device__ void mma_issuer(const Params &p, Shared &sh, uint8_t *sQ, uint8_t *sKV) {
     using C = Cfg<D, DOC, F8>;
     volatile int *abort = &sh.abort;
@@ -483,7 +589,7 @@ __device__ void mma_issuer(const Params &p, Shared &sh, uint8_t *sQ, uint8_t *sK
 
     FOR_EACH_UNIT(u) {
         Unit w;
-        if (!get_unit<PAGED, SINK>(u, p, w)) continue;
+        if (!get_unit<PAGED, SINK, CROSS>(u, p, w)) continue;
         bool first_pv[2] = {true, true};
         for (int t = 0; t < 2; ++t) {
             if (w.lo[t] >= w.hi[t]) continue;
@@ -609,7 +715,7 @@ __device__ __forceinline__ void exp_half_f8(const float (&v)[kHalf], float sl2, 
 }
 
 // ---------------------------------------------------------------- softmax
-template <int D, bool PAGED, bool DOC, bool F8, bool SINK>
+template <int D, bool PAGED, bool DOC, bool F8, bool SINK, bool CROSS>
 __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
     using C = Cfg<D, DOC, F8>;
     volatile int *abort = &sh.abort;
@@ -623,13 +729,24 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
 
     FOR_EACH_UNIT(u) {
         Unit w;
-        if (!get_unit<PAGED, SINK>(u, p, w)) continue;
+        if (!get_unit<PAGED, SINK, CROSS>(u, p, w)) continue;
         // (selects, not w.lo[t]: a run-time index would keep the unit in
         // local memory)
         const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
         const int ns = SINK ? (t ? w.ns[1] : w.ns[0]) : 0;   // sink blocks before lo
-        if (lo >= hi) continue;
         const int row = w.q0 + t * kBlockM + r;    // row index within the sequence
+        if (lo >= hi) {
+            if (CROSS && row < w.L) {              // no key at all: O = 0, LSE = -inf
+                const size_t at = ((size_t)(w.tok0 + row) * p.Hq + w.h) * D;
+                char *dst = static_cast<char *>(p.o) + at * (p.o_fp32 ? 4 : 2);
+                for (int c = 0; c < D * (p.o_fp32 ? 4 : 2); c += 16)
+                    *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+                if (p.lse)
+                    p.lse[p.cu_seqlens ? (size_t)w.h * p.total_tokens + w.tok0 + row
+                                       : ((size_t)w.seq * p.Hq + w.h) * p.seqlen + row] = -INFINITY;
+            }
+            continue;
+        }
         const int rmin = w.q0 + t * kBlockM, rmax = rmin + kBlockM - 1;
         // Document mask: this row's id, and the key ids of the next block
         // (lane l holds keys 4l .. 4l+3), loaded one block ahead; ids past the
@@ -676,7 +793,7 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
             const int k0 = j * kBlockN;
             // keys of the sequence and the key position of query row 0:
             // L and 0 for dense and packed batches
-            const int Lk = PAGED ? w.Lk : w.L;
+            const int Lk = (PAGED || CROSS) ? w.Lk : w.L;
             const int off = PAGED ? w.off : 0;
             const bool edge = (k0 + kBlockN > Lk) ||
                               (p.causal && k0 + kBlockN - 1 > off + rmin) ||
@@ -859,12 +976,13 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
     }
 }
 
-template <int D, bool PAGED, bool DOC, bool F8, bool SINK = false>
+template <int D, bool PAGED, bool DOC, bool F8, bool SINK = false, bool CROSS = false>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const Params p) {
     static_assert(!F8 || (D == 128 && !PAGED && !DOC), "FP8: dense batches, d = 128");
     static_assert(!SINK || (!PAGED && !DOC && !F8), "sink tokens: bf16 dense and packed batches");
+    static_assert(!CROSS || (!PAGED && !DOC && !F8 && !SINK), "cross attention: bf16, no mask");
     using C = Cfg<D, DOC, F8>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared sh;
@@ -889,6 +1007,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             mbar_init(&sh.kv_empty[s], 1);
         }
         mbar_init(&sh.drain, 1);
+        mbar_init(&sh.v_tail, 1);
         sh.abort = 0;
         fence_barrier_init();
     }
@@ -904,17 +1023,19 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
     if (warp < kSoftmaxWarps) {
         regs_increase<kRegsSoftmax>();
-        softmax_wg<D, PAGED, DOC, F8, SINK>(p, sh,
+        softmax_wg<D, PAGED, DOC, F8, SINK, CROSS>(p, sh,
                                       reinterpret_cast<int *>(sKV + C::kStages * C::kTileBytes));
     } else {
         regs_decrease<kRegsControl>();
         if (warp == kWarpTma) {
             if constexpr (PAGED)
                 producer_paged<D>(&tmQ, &tmK, &tmV, p, sh, sQ, sKV);
+            else if constexpr (CROSS)
+                producer_cross<D>(&tmQ, &tmK, &tmV, p, sh, sQ, sKV);
             else if (lane_id() == 0)
                 producer<D, DOC, F8, SINK>(&tmQ, &tmK, &tmV, p, sh, sQ, sKV);
         } else if (warp == kWarpMma) {
-            if (lane_id() == 0) mma_issuer<D, PAGED, DOC, F8, SINK>(p, sh, sQ, sKV);
+            if (lane_id() == 0) mma_issuer<D, PAGED, DOC, F8, SINK, CROSS>(p, sh, sQ, sKV);
         }
     }
     __syncwarp();
@@ -934,18 +1055,19 @@ static_assert(Cfg<128, true>::kSmemBytes + sizeof(Shared) <= 232448, "shared mem
 static_assert(Cfg<64, true>::kSmemBytes + sizeof(Shared) <= 232448, "shared memory");
 static_assert(Cfg<128, false, true>::kSmemBytes + sizeof(Shared) <= 232448, "shared memory");
 
-template <int D, bool PAGED, bool DOC, bool F8 = false, bool SINK = false>
+template <int D, bool PAGED, bool DOC, bool F8 = false, bool SINK = false, bool CROSS = false>
 int launch_kernel(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                   const Params &p, long long units, cudaStream_t stream) {
     using C = Cfg<D, DOC, F8>;
     // Setting the attribute is idempotent and cheap; do it on every call so
     // that any device the caller switches to is covered.
-    if (cudaFuncSetAttribute(prefill_kernel<D, PAGED, DOC, F8, SINK>,
+    if (cudaFuncSetAttribute(prefill_kernel<D, PAGED, DOC, F8, SINK, CROSS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
         cudaSuccess)
         return -5;
     const int grid = (int)(units < device_sm_count() ? units : device_sm_count());
-    prefill_kernel<D, PAGED, DOC, F8, SINK><<<grid, kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
+    prefill_kernel<D, PAGED, DOC, F8, SINK, CROSS><<<grid, kThreads, C::kSmemBytes, stream>>>(tq, tk,
+                                                                                         tv, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
@@ -975,6 +1097,10 @@ Params make_params(const PrefillArgs &a) {
     p.num_pages = a.num_pages;
     p.num_mblocks = (a.max_seqlen + 2 * kBlockM - 1) / (2 * kBlockM);
     p.n_sink = a.n_sink;
+    p.cu_seqlens_k = a.cu_seqlens_k;
+    p.seqlen_k = a.seqlen_k;
+    p.total_k = a.total_k;
+    p.max_seqlen_k = a.max_seqlen_k;
     return p;
 }
 
@@ -984,13 +1110,17 @@ int launch_d(const PrefillArgs &a, cudaStream_t stream) {
     const uint64_t T = (uint64_t)a.total_tokens;
     // K/V: the packed tokens (dense, varlen), or the cache's num_pages * 16
     // rows read one 16-row page box at a time (paged)
-    const uint64_t TK = a.paged ? (uint64_t)a.num_pages * kPageRows : T;
+    const uint64_t TK = a.paged ? (uint64_t)a.num_pages * kPageRows
+                        : a.cross ? (uint64_t)(a.total_k > 0 ? a.total_k : 1) : T;
+    // (cross attention without any key never uses the K and V maps: any valid address)
+    const bool no_keys = a.cross && a.total_k == 0;
+    const void *k = no_keys ? a.q : a.k, *v = no_keys ? a.q : a.v;
     const uint32_t kv_box = a.paged ? kPageRows : kBlockN;
     if (encode_tensor_map_3d(&tq, a.q, 2, D, a.Hq, T, (uint64_t)D * 2, (uint64_t)a.Hq * D * 2,
                              64, 1, kBlockM, 128) ||
-        encode_tensor_map_3d(&tk, a.k, 2, D, a.Hkv, TK, (uint64_t)D * 2, (uint64_t)a.Hkv * D * 2,
+        encode_tensor_map_3d(&tk, k, 2, D, a.Hkv, TK, (uint64_t)D * 2, (uint64_t)a.Hkv * D * 2,
                              64, 1, kv_box, 128) ||
-        encode_tensor_map_3d(&tv, a.v, 2, D, a.Hkv, TK, (uint64_t)D * 2, (uint64_t)a.Hkv * D * 2,
+        encode_tensor_map_3d(&tv, v, 2, D, a.Hkv, TK, (uint64_t)D * 2, (uint64_t)a.Hkv * D * 2,
                              64, 1, kv_box, 128))
         return -5;
     Params p = make_params(a);
@@ -999,6 +1129,7 @@ int launch_d(const PrefillArgs &a, cudaStream_t stream) {
     if (units > (1ll << 30)) return -2;
     p.num_units = (int)units;
     if (a.paged) return launch_kernel<D, true, false>(tq, tk, tv, p, units, stream);
+    if (a.cross) return launch_kernel<D, false, false, false, false, true>(tq, tk, tv, p, units, stream);
     if (a.doc) return launch_kernel<D, false, true>(tq, tk, tv, p, units, stream);
     if (a.n_sink > 0 && a.causal && a.window > 0)
         return launch_kernel<D, false, false, false, true>(tq, tk, tv, p, units, stream);

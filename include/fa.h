@@ -237,6 +237,58 @@ int fa_bwd_varlen(const void *q, const void *k, const void *v, const void *o,
                   void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Cross attention: queries attend to keys and values of another length, an
+ * encoder's states ("What attention costs": the same softmax(QK^T/sqrt d)V,
+ * with N_q x N_k scores and no causal order between them).  Every query of a
+ * sequence sees every visible key of it.
+ *
+ * fa_fwd_cross, dense:
+ *   q [B, Nq, Hq, d], k and v [B, Nk, Hkv, d] bf16, device
+ *   o [B, Nq, Hq, d] bf16 or fp32, written; lse [B, Hq, Nq] fp32 or NULL
+ *   seq_lens_k [B] int32, device, or NULL (all Nk): the first seq_lens_k[b]
+ *             keys of sequence b are visible (an encoder's padded batch); the
+ *             rows behind them may hold anything, NaN included.
+ * fa_fwd_varlen_cross, packed:
+ *   q [total_q, Hq, d] by cu_seqlens_q, k and v [total_k, Hkv, d] by
+ *   cu_seqlens_k ([num_seqs + 1] int32 each, device, as in fa_fwd_varlen);
+ *   o [total_q, Hq, d]; lse [Hq, total_q] or NULL; max_seqlen_q and
+ *   max_seqlen_k no smaller than any length.
+ * A sequence without a visible key gets O = 0, LSE = -inf.  Rows of q, k or v
+ * that belong to no sequence may hold anything, and rows of o and lse that do
+ * are left as they were.  A sequence whose offsets or length do not fit is
+ * skipped (its rows unwritten) and reported through fa_check_device_error as
+ * FA_ERR_INVALID_ARG.  Other arguments and errors as for fa_fwd.
+ *
+ * fa_bwd_cross, fa_bwd_varlen_cross: the gradients, as fa_bwd gives them, of
+ * sum(dO * O) with respect to Q, K and V.
+ *   o, dout, dq like q; dk, dv like k; lse the forward's (required)
+ *   dk, dv rows of keys that no query sees (behind seq_lens_k, or of a
+ *   sequence without queries) are written as zeros, and so are dq rows of a
+ *   sequence without keys; packed rows that belong to no sequence are left as
+ *   they were.  dq rows of a skipped sequence are written as zeros.
+ *   workspace: fa_bwd_workspace_bytes(B * Nq or total_q, Hq, d) bytes, 256-byte
+ *   aligned, not to be shared by calls that may overlap on the GPU.
+ * dQ is accumulated in fp32 with atomic adds (its last bits may differ from
+ * run to run); dK and dV are deterministic.
+ */
+int fa_fwd_cross(const void *q, const void *k, const void *v, void *o, float *lse,
+                 const int *seq_lens_k, int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale,
+                 int o_dtype, void *stream);
+int fa_fwd_varlen_cross(const void *q, const void *k, const void *v, void *o, float *lse,
+                        const int *cu_seqlens_q, const int *cu_seqlens_k, int num_seqs, int total_q,
+                        int total_k, int max_seqlen_q, int max_seqlen_k, int Hq, int Hkv, int d,
+                        float scale, int o_dtype, void *stream);
+int fa_bwd_cross(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                 const float *lse, void *dq, void *dk, void *dv, const int *seq_lens_k, int B, int Hq,
+                 int Hkv, int Nq, int Nk, int d, float scale, void *workspace,
+                 size_t workspace_bytes, void *stream);
+int fa_bwd_varlen_cross(const void *q, const void *k, const void *v, const void *o,
+                        const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                        const int *cu_seqlens_q, const int *cu_seqlens_k, int num_seqs, int total_q,
+                        int total_k, int max_seqlen_q, int max_seqlen_k, int Hq, int Hkv, int d,
+                        float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Bytes of workspace fa_decode_paged needs for these sizes (split-KV
  * partial outputs and their log-sum-exps).  0 for an invalid combination.
  */
