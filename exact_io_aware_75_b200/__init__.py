@@ -16,6 +16,8 @@ Functions mirror the C entry points:
     fwd_fp8        -> fa_fwd_fp8        (FP8 prefill on those operands)
     fwd_cross, fwd_varlen_cross, bwd_cross, bwd_varlen_cross
                    -> fa_*_cross        (cross attention and its backward)
+    decode_shared  -> fa_decode_shared  (paged decode with shared prefixes)
+    decode_cross   -> fa_decode_cross   (few queries against encoder states)
     cache_fork, cache_append, cache_copy_pages, cache_collect, cache_compact
                    -> fa_cache_*        (the pages of the cache)
     decode_paged_noalloc, decode_workspace_bytes, bwd_workspace_bytes,
@@ -51,6 +53,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_varlen", "fa_fwd_sinks", "fa_fwd_varlen_sinks", "fa
            "fa_decode_workspace_bytes", "fa_decode_paged", "fa_decode_paged_sinks",
            "fa_decode_paged_fp8", "fa_fp8_workspace_bytes", "fa_fp8_prepare", "fa_fwd_fp8",
            "fa_fwd_cross", "fa_fwd_varlen_cross", "fa_bwd_cross", "fa_bwd_varlen_cross",
+           "fa_decode_shared_workspace_bytes", "fa_decode_shared",
+           "fa_decode_cross_workspace_bytes", "fa_decode_cross",
            "fa_cache_fork", "fa_cache_append", "fa_cache_copy_pages",
            "fa_cache_collect_workspace_bytes", "fa_cache_collect",
            "fa_cache_compact_workspace_bytes", "fa_cache_compact",
@@ -121,6 +125,14 @@ def _load():
     lib.fa_bwd_cross.restype = i
     lib.fa_bwd_varlen_cross.argtypes = [vp] * 11 + [i] * 8 + [f, vp, sz, vp]
     lib.fa_bwd_varlen_cross.restype = i
+    lib.fa_decode_shared_workspace_bytes.argtypes = [i] * 4
+    lib.fa_decode_shared_workspace_bytes.restype = sz
+    lib.fa_decode_shared.argtypes = [vp] * 10 + [i] * 8 + [f, vp, sz, vp]
+    lib.fa_decode_shared.restype = i
+    lib.fa_decode_cross_workspace_bytes.argtypes = [i] * 5
+    lib.fa_decode_cross_workspace_bytes.restype = sz
+    lib.fa_decode_cross.argtypes = [vp] * 6 + [i] * 6 + [f, vp, sz, vp]
+    lib.fa_decode_cross.restype = i
     lib.fa_cache_fork.argtypes = ([vp] * 4 + [i, vp, vp, i, vp, i, vp, vp, i] + [vp] * 3 + [i] * 5
                                   + [vp])
     lib.fa_cache_fork.restype = i
@@ -467,6 +479,13 @@ def _out_pair(out, lse, o_shape, lse_shape, out_dtype, return_lse, device):
     return out, lse, FA_OUT_FP32 if out.dtype == torch.float32 else FA_OUT_BF16
 
 
+def _decode_out(out, lse, o_shape, lse_shape, return_lse, device):
+    """As _out_pair, for calls whose O is bf16."""
+    if out is not None and getattr(out, "dtype", None) != torch.bfloat16:
+        raise FAError(FA_ERR_INVALID_ARG, "out must be torch.bfloat16")
+    return _out_pair(out, lse, o_shape, lse_shape, torch.bfloat16, return_lse, device)[:2]
+
+
 def _same(t, ref, name):
     """A tensor of ref's type and shape."""
     _need(t, ref.dtype, ref.dim(), name)
@@ -583,6 +602,76 @@ def bwd_varlen_cross(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seql
                                         workspace.numel() * workspace.element_size(),
                                         _stream(stream)), "fa_bwd_varlen_cross")
     return dq, dk, dv
+
+
+def decode_shared_workspace_bytes(num_seqs, Hq, Hkv, d) -> int:
+    return int(_lib.fa_decode_shared_workspace_bytes(int(num_seqs), int(Hq), int(Hkv), int(d)))
+
+
+def decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, scale=None,
+                  sinks=None, out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """Paged decode of sequences that share prefixes.  q [S,Hq,d], caches [P,16,Hkv,d],
+    block_table [S,maxp], seq_lens [S], cu_groups [G+1], prefix_lens [G] int32: the sequences
+    of group g name the same pages for their first prefix_lens[g] // 16 table entries
+    -> (O [S,Hq,d] bf16, LSE [S,Hq])."""
+    _need(q, torch.bfloat16, 3, "q")
+    _need(k_cache, torch.bfloat16, 4, "k_cache")
+    _need(v_cache, torch.bfloat16, 4, "v_cache")
+    _need(block_table, torch.int32, 2, "block_table")
+    S, Hq, d = q.shape
+    P, ps, Hkv, dk = k_cache.shape
+    maxp = block_table.shape[1]
+    if v_cache.shape != k_cache.shape or dk != d or block_table.shape[0] != S:
+        raise FAError(FA_ERR_INVALID_ARG, "shapes")
+    _need_ints((S,), "seq_lens", seq_lens)
+    _need(prefix_lens, torch.int32, 1, "prefix_lens")
+    groups = prefix_lens.shape[0]
+    _need_ints((groups + 1,), "cu_groups", cu_groups)
+    if sinks is not None:
+        _need(sinks, torch.float32, 1, "sinks")
+        if sinks.shape[0] != Hq:
+            raise FAError(FA_ERR_INVALID_ARG, "sinks shape")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out, lse = _decode_out(out, lse, (S, Hq, d), (S, Hq), return_lse, q.device)
+    workspace = _bytes_of(workspace, decode_shared_workspace_bytes(S, Hq, max(Hkv, 1), d), q.device)
+    with _device_of(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                    seq_lens=seq_lens, cu_groups=cu_groups, prefix_lens=prefix_lens, sinks=sinks,
+                    out=out, lse=lse, workspace=workspace):
+        _check(_lib.fa_decode_shared(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                     _ptr(seq_lens), _ptr(cu_groups), _ptr(prefix_lens),
+                                     _ptr(out), _ptr(lse), _ptr(sinks), S, groups, P, Hq, Hkv, d,
+                                     ps, maxp, float(scale), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(),
+                                     _stream(stream)), "fa_decode_shared")
+    return out, lse
+
+
+def decode_cross_workspace_bytes(B, Hq, Hkv, Nq, d) -> int:
+    return int(_lib.fa_decode_cross_workspace_bytes(int(B), int(Hq), int(Hkv), int(Nq), int(d)))
+
+
+def decode_cross(q, k, v, seq_lens_k=None, scale=None, out=None, lse=None, return_lse=True,
+                 workspace=None, stream=None):
+    """Cross attention of few queries, the keys split over the GPU.  q [B,Nq,Hq,d], k/v
+    [B,Nk,Hkv,d] bf16, seq_lens_k [B] int32 (device) or None -> (O [B,Nq,Hq,d] bf16,
+    LSE [B,Hq,Nq])."""
+    _cross_shapes(q, k, v, 4)
+    B, Nq, Hq, d = q.shape
+    Nk, Hkv = k.shape[1:3]
+    if seq_lens_k is not None:
+        _need_ints((B,), "seq_lens_k", seq_lens_k)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out, lse = _decode_out(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), return_lse, q.device)
+    workspace = _bytes_of(workspace, decode_cross_workspace_bytes(B, Hq, max(Hkv, 1), Nq, d),
+                          q.device)
+    with _device_of(q, k=k, v=v, seq_lens_k=seq_lens_k, out=out, lse=lse, workspace=workspace):
+        _check(_lib.fa_decode_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens_k), _ptr(out),
+                                    _ptr(lse), B, Hq, Hkv, Nq, Nk, d, float(scale),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(stream)), "fa_decode_cross")
+    return out, lse
 
 
 def decode_workspace_bytes(num_seqs, Hq, d, page_size, max_pages_per_seq) -> int:

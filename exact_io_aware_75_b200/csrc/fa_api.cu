@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -902,6 +903,128 @@ int fa_bwd_varlen_cross(const void *q, const void *k, const void *v, const void 
     return bwd_cross_call(q, k, v, o, dout, lse, dq, dk, dv, nullptr, cu_seqlens_q, cu_seqlens_k,
                           true, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hkv, d,
                           scale, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int kSharedMaxGroup = 128;   // query heads per KV head
+
+// Sequences that one launch of decode_cross takes: blocks of 256 rows bound it.
+int cross_batch(int B, long long rows_per_seq) {
+    const long long pairs = (rows_per_seq + 255) / 256;
+    const long long most = fa::kSharedMaxItems / pairs;
+    return (int)std::min<long long>(B, std::min<long long>(most, fa::kSharedMaxSeqs));
+}
+
+// Sizes decode_cross can take: rows of a sequence in one launch's items, and
+// the plan's cost (below) within 32 bits.
+bool cross_fits(int Hq, int Hkv, int Nq, int Nk) {
+    const int G = Hq / Hkv;
+    const long long rows = (long long)Nq * G;
+    return G <= kSharedMaxGroup && rows <= 256ll * fa::kSharedMaxItems &&
+           fa::kSharedMaxItems * 4ll * (Nk / 128 + 2) <= INT32_MAX / 2;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_decode_shared_workspace_bytes(int num_seqs, int Hq, int Hkv, int d) {
+    if (num_seqs <= 0 || num_seqs > fa::kSharedMaxSeqs || Hkv <= 0 || Hq <= 0 || Hq % Hkv ||
+        Hq / Hkv > kSharedMaxGroup || (d != 64 && d != 128))
+        return 0;
+    return fa::shared_workspace_bytes((long long)num_seqs * (Hq / Hkv), Hkv, d, true);
+}
+
+int fa_decode_shared(const void *q, const void *k_cache, const void *v_cache,
+                     const int *block_table, const int *seq_lens, const int *cu_groups,
+                     const int *prefix_lens, void *o, float *lse, const float *sinks, int num_seqs,
+                     int num_groups, int num_pages, int Hq, int Hkv, int d, int page_size,
+                     int max_pages_per_seq, float scale, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    if (num_seqs < 0 || num_groups < 0 || num_groups > num_seqs || num_pages < 0 ||
+        max_pages_per_seq <= 0)
+        return FA_ERR_INVALID_ARG;
+    int rc = check_common(Hq, Hkv, d, 0, 0, scale, FA_OUT_BF16);
+    if (rc) return rc;
+    const int G = Hq / Hkv;
+    if (page_size != 16 || num_seqs > fa::kSharedMaxSeqs || G > kSharedMaxGroup)
+        return FA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return FA_OK;
+    if (num_pages == 0) return FA_ERR_INVALID_ARG;
+    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o ||
+        (num_groups > 0 && (!cu_groups || !prefix_lens)))
+        return FA_ERR_INVALID_ARG;
+    // 32-bit row coordinates, page counts and plan costs (at most 3 per block of 8 pages and item)
+    const long long items = 2ll * num_seqs + (long long)num_seqs * G / 256 + 1;
+    if ((long long)num_pages * page_size > INT32_MAX / 2 || max_pages_per_seq >= 1 << 22 ||
+        items * 4 * (max_pages_per_seq / 8 + 2) > INT32_MAX / 2)
+        return FA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
+        !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_groups) ||
+        !aligned4(prefix_lens) || !aligned4(lse) || !aligned4(sinks))
+        return FA_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < fa_decode_shared_workspace_bytes(num_seqs, Hq, Hkv, d))
+        return FA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return FA_ERR_ALIGNMENT;
+    fa::SharedArgs a{};
+    a.q = q; a.k = k_cache; a.v = v_cache;
+    a.block_table = block_table; a.lens = seq_lens;
+    a.cu_groups = cu_groups; a.prefix_lens = prefix_lens;
+    a.o = o; a.lse = lse; a.sinks = sinks;
+    a.paged = 1;
+    a.S = num_seqs;
+    a.num_groups = num_groups;
+    a.num_pages = num_pages; a.max_pages = max_pages_per_seq;
+    a.Hq = Hq; a.Hkv = Hkv; a.d = d; a.Nq = 1;
+    a.scale = scale;
+    a.workspace = workspace; a.workspace_bytes = workspace_bytes;
+    return map_rc(fa::launch_shared(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_decode_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
+    if (B <= 0 || Nq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || (d != 64 && d != 128) ||
+        !cross_fits(Hq, Hkv, Nq, 0))
+        return 0;
+    const long long rows = (long long)Nq * (Hq / Hkv);
+    return fa::shared_workspace_bytes(cross_batch(B, rows) * rows, Hkv, d, false);
+}
+
+int fa_decode_cross(const void *q, const void *k, const void *v, const int *seq_lens_k, void *o,
+                    float *lse, int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale,
+                    void *workspace, size_t workspace_bytes, void *stream) {
+    if (B < 0 || Nq < 0 || Nk < 0) return FA_ERR_INVALID_ARG;
+    int rc = check_common(Hq, Hkv, d, 0, 0, scale, FA_OUT_BF16);
+    if (rc) return rc;
+    if (B == 0 || Nq == 0) return FA_OK;
+    rc = check_cross(q, k, v, o, lse, seq_lens_k, nullptr, nullptr, false, (long long)B * Nq,
+                     (long long)B * Nk);
+    if (rc) return rc;
+    if (!cross_fits(Hq, Hkv, Nq, Nk)) return FA_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < fa_decode_cross_workspace_bytes(B, Hq, Hkv, Nq, d))
+        return FA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return FA_ERR_ALIGNMENT;
+    const int batch = cross_batch(B, (long long)Nq * (Hq / Hkv));
+    for (int s0 = 0; s0 < B; s0 += batch) {    // (one launch after the other uses the workspace)
+        const size_t q0 = (size_t)s0 * Nq * Hq, k0 = (size_t)s0 * Nk * Hkv * d * 2;
+        fa::SharedArgs a{};
+        a.q = static_cast<const char *>(q) + q0 * d * 2;
+        a.k = k ? static_cast<const char *>(k) + k0 : nullptr;
+        a.v = v ? static_cast<const char *>(v) + k0 : nullptr;
+        a.lens = seq_lens_k ? seq_lens_k + s0 : nullptr;
+        a.o = static_cast<char *>(o) + q0 * d * 2;
+        a.lse = lse ? lse + q0 : nullptr;
+        a.S = std::min(batch, B - s0);
+        a.S_all = B - s0;
+        a.Hq = Hq; a.Hkv = Hkv; a.d = d; a.Nq = Nq; a.Nk = Nk;
+        a.scale = scale;
+        a.workspace = workspace; a.workspace_bytes = workspace_bytes;
+        rc = map_rc(fa::launch_shared(a, static_cast<cudaStream_t>(stream)));
+        if (rc) return rc;
+    }
+    return FA_OK;
 }
 
 const char *fa_status_string(int status) {

@@ -81,6 +81,27 @@ bool decode_tc_supported(const DecodeArgs &a);
 int launch_decode_split_tc(const DecodeArgs &a, float *part_o, float *part_lse, int max_chunks,
                            cudaStream_t stream);
 
+// Attention of many rows to common keys (shared_sm100.cu): decode over a paged
+// cache with shared prefixes (paged), or of Nq tokens per sequence against
+// stored keys [S_all, Nk] (S sequences of them in this launch).
+constexpr int kSharedMaxSeqs = 1024;   // sequences per launch
+constexpr int kSharedMaxItems = 2048;  // blocks of 256 query rows per launch
+constexpr int kSharedMaxCtas = 160;    // CTAs a launch may have (and the workspace has room for)
+struct SharedArgs {
+    const void *q, *k, *v;
+    const int *block_table, *lens, *cu_groups, *prefix_lens;
+    void *o;
+    float *lse;
+    const float *sinks;
+    int paged, S, S_all, num_groups, num_pages, max_pages, Hq, Hkv, d, Nq, Nk;
+    float scale;
+    void *workspace;
+    size_t workspace_bytes;
+};
+
+size_t shared_workspace_bytes(long long rows_per_kvh, int Hkv, int d, bool paged);
+int launch_shared(const SharedArgs &a, cudaStream_t stream);
+
 // Sizes the backward launch needs; validated by the public entry points.
 struct BwdArgs {
     const void *q, *k, *v, *o, *dout;

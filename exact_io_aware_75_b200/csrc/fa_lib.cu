@@ -5,6 +5,7 @@
 #include "decode_tc_sm100.cu"
 #include "decode_sm100.cu"
 #include "decode_noalloc.cu"
+#include "shared_sm100.cu"
 #include "bwd_sm100.cu"
 #include "fp8_prep.cu"
 #include "cache_pages.cu"

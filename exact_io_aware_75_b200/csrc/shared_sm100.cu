@@ -1,0 +1,1116 @@
+// shared_sm100.cu -- attention of many query rows to one set of keys, split
+// over the keys: decode of a batch whose sequences share a prefix, and decode
+// against an encoder's states.
+//
+// What it computes: O = softmax(Q K^T * scale) V and LSE of every query row,
+// all keys visible up to a length.  The softmax over several sets of keys
+// r = 1, 2, ... (the shared pages, the sequence's own pages, pieces of
+// either) is joined from the sets' own results:
+//     M = max_r LSE_r,  O = sum_r 2^(LSE_r - M) O_r / sum_r 2^(LSE_r - M).
+//
+// How:
+//   * The work is a list of items.  An item is up to 256 query rows and the
+//     keys they all see: the rows (sequence, head of the KV head's group) of a
+//     group of sequences on the group's shared pages, so that these cross HBM
+//     once and not once per sequence; the group's heads of one sequence on
+//     the sequence's own pages; the tokens and heads of one sequence on its
+//     encoder states.  All items exist once per KV head.
+//   * Every KV head gets the same number n of CTAs (n * Hkv of the SMs), and
+//     each of them an equal share of the items' key blocks, cut anywhere:
+//     with lengths from one token to many thousand every SM still ends at the
+//     same time.  CTAs of the KV heads at the same place read the same tokens
+//     at the same time, so that whole token rows cross HBM together.  A share
+//     gives one partial (fp32 O, LSE) per row and item it touches.  The plan
+//     (prefix sums over the items) is computed by every CTA for itself in
+//     shared memory, about two microseconds; lengths never come to the host.
+//   * Warp 8 feeds a ring of K and V tiles (128 keys) by TMA, page by page
+//     through the block table, and runs ahead over the items.  Warp 9 issues
+//     the products S = Q K^T and O += P V (tcgen05, O in tensor memory).  Warp
+//     10 clears the V rows behind a sequence's end (they may hold anything,
+//     and P = 0 times NaN is NaN).
+//   * Two softmax warpgroups.  More than 128 rows: each has a tile of 128
+//     rows and sees every key block (as the prefill).  Fewer: both have the
+//     same rows and take the key blocks in turn.  At 64 rows or fewer the
+//     rows stand two or four times in the tile's 128 lanes: a warp can read
+//     only its own 32 lanes of tensor memory, so copy i of the rows takes the
+//     i-th part of each block's keys (P = 0 in the others'), and the
+//     exponentials of 4 rows x 128 keys are spread over four warps instead of
+//     one.  The tensor core would compute the other lanes anyway.  The
+//     copies' and the warpgroups' results are joined through shared memory.
+//   * shared_combine_kernel joins the partials of each row.
+#include <climits>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+#include "sm100.cuh"
+
+namespace fa {
+
+namespace shared_impl {
+
+constexpr int kPage = 16;           // tokens per cache page
+constexpr int kBlockM = 128;        // rows per tile (TMEM lanes)
+constexpr int kBlockN = 128;        // keys per K/V tile
+constexpr int kPagesPerBlock = kBlockN / kPage;
+constexpr int kRows = 2 * kBlockM;  // rows per item
+constexpr int kThreads = 384;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpClear = 10;
+// Registers: launched with 384 x 168; softmax warpgroups 216, the rest 72
+// (2 * 128 * 216 + 128 * 72 = 64,512).
+constexpr int kRegsSoftmax = 216, kRegsControl = 72;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsControl <= kThreads * 168, "register split");
+constexpr float kRescaleThreshold = 8.0f;   // log2 units, as in the prefill
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxSeqs = kSharedMaxSeqs;    // sequences per launch
+constexpr int kMaxGroupItems = 1024;        // group <= 128 heads: at most S/2 + S/2 items
+constexpr int kMaxItems = kSharedMaxItems;
+static_assert(kMaxSeqs + kMaxGroupItems <= kMaxItems, "items of a paged batch");
+// Cost of a key block, in half tiles of K/V read from HBM, and of an item
+// besides (its first loads and its epilogue).
+constexpr int kCostBlock = 2, kCostBlock2 = 3, kCostItem = 1;
+
+template <int D>
+struct Cfg {
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kBoxBytes = kBlockM * 128;            // 128 rows x 128 bytes
+    static constexpr int kTileBytes = kBlockM * D * 2;
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kOffKV = 2 * kTileBytes;
+    static constexpr int kOffTable = kOffKV + kStages * kTileBytes;
+    static constexpr uint32_t kColO = 256;                     // O_t at 256 + t*D
+    static constexpr int kChunk = D == 128 ? 32 : 16;          // columns joined at a time
+};
+
+// The plan, in shared memory.
+struct Table {
+    int start[kMaxItems];      // cost before the item
+    int slot[kMaxItems];       // partial rows before the item
+    int2 gi[kMaxGroupItems];   // group items: first sequence | count << 16, pages | row pair << 22
+    int own[kMaxSeqs];         // pages of each sequence that its group reads
+    int num_group_items, num_items, span;
+};
+
+struct Params {
+    const uint16_t *q;
+    const int *block_table, *lens, *cu_groups, *prefix_lens;
+    float *part_o, *part_lse;  // [Hkv][cap][D], [Hkv][cap], log2 units
+    int4 *items;               // {slot, partials, rows, -}
+    int4 *seqs;                // {own item, first group item or -1, group's first sequence, -}
+    int S, num_groups, num_pages, max_pages;
+    int Hq, Hkv, G, Nq, Nk, pairs;
+    int n;                     // CTAs per KV head
+    int total_k;               // dense: stored key rows
+    long long cap;
+    float scale_log2;
+};
+
+struct Shared {
+    uint64_t q_full[2];
+    uint64_t kv_full[8], kv_empty[8], tail[8];
+    uint64_t s_full[2], p_lo[2], p_hi[2], o_full[2], o_empty[2];
+    uint64_t drain;
+    float2 ml[8][32];
+    int scan[kThreads / 32];
+    uint32_t tmem_base;
+    int abort;
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+template <bool PAGED>
+__device__ __forceinline__ int length_of(const Params &p, int s, bool report) {
+    const int most = PAGED ? p.max_pages * kPage : p.Nk;
+    int L = p.lens ? __ldg(p.lens + s) : most;
+    if (L < 0 || L > most) {
+        if (report) report_error(kDevErrInput);
+        L = L < 0 ? 0 : most;
+    }
+    return L;
+}
+
+// One item: which rows, which keys.
+struct Item {
+    int tok0;        // token of row 0 of the rows' set
+    int row0, rows;  // the item's rows of that set
+    int src;         // sequence whose block table (or key rows) it reads
+    int page0;       // paged: first page
+    int keys;
+};
+
+template <bool PAGED>
+__device__ __forceinline__ Item get_item(const Params &p, const Table &tab, int i) {
+    Item w;
+    int all = p.Nq * p.G;
+    w.row0 = 0;
+    w.page0 = 0;
+    if constexpr (PAGED) {
+        if (i < tab.num_group_items) {
+            const int2 g = tab.gi[i];
+            w.tok0 = w.src = g.x & 0xffff;
+            all = (g.x >> 16) * p.G;
+            w.row0 = (g.y >> 22) * kRows;
+            w.keys = (g.y & 0x3fffff) * kPage;
+        } else {
+            w.tok0 = w.src = i - tab.num_group_items;
+            w.page0 = tab.own[w.src];
+            w.keys = max(0, length_of<true>(p, w.src, false) - w.page0 * kPage);
+        }
+    } else {
+        w.src = i / p.pairs;
+        w.tok0 = w.src * p.Nq;
+        w.row0 = (i % p.pairs) * kRows;
+        w.keys = length_of<false>(p, w.src, false);
+    }
+    w.rows = min(kRows, all - w.row0);
+    return w;
+}
+
+__device__ __forceinline__ int block_cost(int rows) { return rows > kBlockM ? kCostBlock2 : kCostBlock; }
+
+// Exclusive prefix sum over the block's threads; `total` gets the sum.
+__device__ __forceinline__ int block_scan(int x, int *s_warp, int &total) {
+    const int lane = lane_id(), warp = warp_id();
+    int inc = x;
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    #pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+    }
+    return before + inc - x;
+}
+
+// All threads of the block; ends with a barrier.  `scratch`: room for
+// 3 * kMaxSeqs + 1 ints.
+template <bool PAGED>
+__device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp) {
+    const int tid = threadIdx.x;
+    const bool lead = blockIdx.x == 0;
+    int ni = 0;
+    if constexpr (PAGED) {
+        int *cu = scratch, *pages = cu + kMaxSeqs + 1, *first = pages + kMaxSeqs;
+        int ng = p.num_groups;
+        for (int g = tid; g <= ng; g += kThreads) {
+            if (ng > 0) cu[g] = __ldg(p.cu_groups + g);
+            if (g < ng) pages[g] = INT_MAX;
+        }
+        __syncthreads();
+        bool bad = false;
+        for (int g = tid; g < ng; g += kThreads)
+            bad |= cu[g] < 0 || cu[g + 1] < cu[g] || cu[g + 1] > p.S;
+        if (__syncthreads_or(bad)) {       // unusable groups: every sequence by itself
+            if (lead && tid == 0) report_error(kDevErrInput);
+            ng = 0;
+        }
+        auto group_of = [&](int s) -> int {
+            int lo = 0, hi = ng;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu[mid] <= s) lo = mid; else hi = mid;
+            }
+            return ng > 0 && cu[lo] <= s && s < cu[lo + 1] ? lo : -1;
+        };
+        // no more is shared than the group's shortest sequence has
+        for (int s = tid; s < p.S; s += kThreads) {
+            const int g = group_of(s), L = length_of<true>(p, s, lead);
+            if (g >= 0) atomicMin(&pages[g], L);
+        }
+        __syncthreads();
+        for (int g0 = 0; g0 < ng; g0 += kThreads) {
+            const int g = g0 + tid;
+            int cnt = 0, pg = 0, items = 0;
+            if (g < ng) {
+                int len = __ldg(p.prefix_lens + g);
+                if (len < 0) {
+                    if (lead) report_error(kDevErrInput);
+                    len = 0;
+                }
+                cnt = cu[g + 1] - cu[g];
+                pg = cnt >= 2 ? min(len, pages[g]) / kPage : 0;
+                items = pg > 0 ? ceil_div(cnt * p.G, kRows) : 0;
+            }
+            int total;
+            const int base = ni + block_scan(items, s_warp, total);
+            ni += total;
+            if (g < ng) {
+                pages[g] = pg;
+                first[g] = pg > 0 ? base : -1;
+                for (int r = 0; r < items; ++r)
+                    tab.gi[base + r] = make_int2(cu[g] | cnt << 16, pg | r << 22);
+            }
+        }
+        __syncthreads();
+        for (int s = tid; s < p.S; s += kThreads) {
+            const int g = group_of(s);
+            tab.own[s] = g >= 0 ? pages[g] : 0;
+            if (lead) p.seqs[s] = make_int4(ni + s, g >= 0 ? first[g] : -1, g >= 0 ? cu[g] : 0, 0);
+        }
+    }
+    const int N = PAGED ? ni + p.S : p.S * p.pairs;
+    if (tid == 0) {
+        tab.num_group_items = ni;
+        tab.num_items = N;
+    }
+    __syncthreads();
+    // cost before each item; a thread has `per` consecutive ones
+    const int per = ceil_div(N, kThreads), i0 = min(N, tid * per), i1 = min(N, i0 + per);
+    int sum = 0, total;
+    for (int i = i0; i < i1; ++i) {
+        const Item w = get_item<PAGED>(p, tab, i);
+        if (!PAGED && lead && w.row0 == 0) length_of<false>(p, w.src, true);
+        tab.start[i] = sum;
+        if (w.keys > 0) sum += ceil_div(w.keys, kBlockN) * block_cost(w.rows) + kCostItem;
+    }
+    const int before = block_scan(sum, s_warp, total);
+    // (every share must hold the start of a block of any item it lies inside)
+    const int span = max(kCostBlock2, ceil_div(total, p.n));
+    int rows = 0;
+    for (int i = i0; i < i1; ++i) {
+        const Item w = get_item<PAGED>(p, tab, i);
+        const int start = tab.start[i] + before;
+        tab.start[i] = start;
+        int parts = 0;
+        if (w.keys > 0) {
+            const int last = start + (ceil_div(w.keys, kBlockN) - 1) * block_cost(w.rows);
+            parts = last / span - start / span + 1;
+        }
+        tab.slot[i] = rows;
+        rows += parts * w.rows;
+    }
+    int all;
+    const int slot0 = block_scan(rows, s_warp, all);
+    for (int i = i0; i < i1; ++i) {
+        tab.slot[i] += slot0;
+        if (lead) {
+            const Item w = get_item<PAGED>(p, tab, i);
+            const int next = i + 1 < i1 ? tab.slot[i + 1] + slot0 : slot0 + rows;
+            p.items[i] = make_int4(tab.slot[i], (next - tab.slot[i]) / w.rows, w.rows, 0);
+        }
+    }
+    if (tid == 0) tab.span = span;
+    __syncthreads();
+}
+
+// One CTA's share of an item.
+struct Work {
+    Item it;
+    int kb0, kb1;    // key blocks
+    int rep;         // copies of the rows in a tile's lanes
+    bool pair;       // two row tiles on every block (else: one, blocks in turn)
+    int slot;        // first partial row
+};
+
+struct Walker {
+    int i, lo, hi;
+    __device__ __forceinline__ void begin(const Params &p, const Table &tab) {
+        const int c = blockIdx.x / p.Hkv;
+        lo = c * tab.span;
+        hi = lo + tab.span;
+        int a = 0, b = tab.num_items;          // the last item that starts at or before lo
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (tab.start[mid] <= lo) a = mid; else b = mid;
+        }
+        i = a;
+    }
+    template <bool PAGED>
+    __device__ __forceinline__ bool next(const Params &p, const Table &tab, Work &w) {
+        for (; i < tab.num_items; ++i) {
+            const int start = tab.start[i];
+            if (start >= hi) return false;
+            w.it = get_item<PAGED>(p, tab, i);
+            const int cost = block_cost(w.it.rows), nb = ceil_div(w.it.keys, kBlockN);
+            w.kb0 = start >= lo ? 0 : min(nb, ceil_div(lo - start, cost));
+            w.kb1 = min(nb, ceil_div(hi - start, cost));
+            if (w.kb0 >= w.kb1) continue;
+            w.pair = w.it.rows > kBlockM;
+            w.rep = w.it.rows > 64 ? 1 : w.it.rows > 32 ? 2 : 4;
+            w.slot = tab.slot[i] + (lo / tab.span - start / tab.span) * w.it.rows;
+            ++i;
+            return true;
+        }
+        return false;
+    }
+};
+
+// V rows behind the item's last key that the copy into shared memory brought:
+// of a page the keys end inside, or (dense) of whatever lies behind.
+template <bool PAGED>
+__device__ __forceinline__ bool needs_clear(const Params &p, const Work &w, int valid) {
+    if (valid >= kBlockN) return false;
+    if (PAGED) return valid % kPage != 0;
+    return (long long)w.it.src * p.Nk + w.it.keys < p.total_k;
+}
+
+// ------------------------------------------------------------- TMA producer
+template <int D, bool PAGED>
+__device__ void producer(const CUtensorMap *tmK, const CUtensorMap *tmV, const Params &p,
+                         const Table &tab, Shared &sh, uint8_t *sKV) {
+    using C = Cfg<D>;
+    volatile int *abort = &sh.abort;
+    const int lane = lane_id(), kvh = blockIdx.x % p.Hkv;
+    uint32_t it = 0, tail_last = 0, tail_phase = 0;
+    Walker walk;
+    walk.begin(p, tab);
+    Work w;
+    while (walk.next<PAGED>(p, tab, w)) {
+        // lane i < 8: page i of a block (-1: behind the keys)
+        auto page_of = [&](int j) -> int {
+            const int c = j * kPagesPerBlock + lane;
+            if (!PAGED || lane >= kPagesPerBlock || j >= w.kb1 || c * kPage >= w.it.keys) return -1;
+            return __ldg(p.block_table + (size_t)w.it.src * p.max_pages + w.it.page0 + c);
+        };
+        int ahead = page_of(w.kb0);
+        for (int j = w.kb0; j < w.kb1; ++j) {
+            int page = ahead;
+            ahead = page_of(j + 1);
+            const int valid = w.it.keys - j * kBlockN;
+            if (PAGED && lane < kPagesPerBlock && lane * kPage < valid &&
+                (page < 0 || page >= p.num_pages)) {
+                report_error(kDevErrInput);
+                page = 0;
+            }
+            const bool clear = needs_clear<PAGED>(p, w, valid);
+            for (int kv = 0; kv < 2; ++kv, ++it) {
+                const int slot = it % C::kStages;
+                const uint32_t bit = 1u << slot;
+                uint8_t *dst = sKV + slot * C::kTileBytes;
+                if (!mbar_wait_warp(&sh.kv_empty[slot], ((it / C::kStages) & 1) ^ 1, abort)) goto out;
+                const bool tail = kv == 1 && clear;
+                uint64_t *bar = tail ? &sh.tail[slot] : &sh.kv_full[slot];
+                tail_last = tail ? tail_last | bit : tail_last & ~bit;
+                if (tail) tail_phase ^= bit;
+                if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
+                __syncwarp();
+                if (PAGED) {
+                    if (lane < kPagesPerBlock) {
+                        // (rows past the cache's extent arrive as zeros)
+                        const int row = page >= 0 ? page * kPage : p.num_pages * kPage;
+                        for (int b = 0; b < C::kBoxes; ++b)
+                            tma_load_3d(dst + b * C::kBoxBytes + lane * kPage * 128, kv ? tmV : tmK,
+                                        bar, b * 64, kvh, row);
+                    }
+                } else if (lane < C::kBoxes) {
+                    tma_load_3d(dst + lane * C::kBoxBytes, kv ? tmV : tmK, bar, lane * 64, kvh,
+                                w.it.src * p.Nk + j * kBlockN);
+                }
+            }
+        }
+    }
+    return;
+out:
+    // Leave no copy in flight: wait for the last load issued into each slot.
+    if (lane == 0)
+        for (int s = 0; s < C::kStages; ++s)
+            if (it > (uint32_t)s) {
+                if (tail_last >> s & 1)
+                    mbar_drain_wait(&sh.tail[s], (tail_phase >> s & 1) ^ 1);
+                else
+                    mbar_drain_wait(&sh.kv_full[s], ((it - 1 - s) / C::kStages) & 1);
+            }
+}
+
+// Warp 10: zeros over the V rows behind an item's last key.
+template <int D, bool PAGED>
+__device__ void clear_tails(const Params &p, const Table &tab, Shared &sh, uint8_t *sKV) {
+    using C = Cfg<D>;
+    const int lane = lane_id();
+    uint32_t it = 0, phase = 0;
+    Walker walk;
+    walk.begin(p, tab);
+    Work w;
+    while (walk.next<PAGED>(p, tab, w)) {
+        const int valid = w.it.keys - (w.kb1 - 1) * kBlockN;
+        it += 2 * (w.kb1 - w.kb0);
+        if (!needs_clear<PAGED>(p, w, valid)) continue;
+        const int slot = (it - 1) % C::kStages;       // the share's last V tile
+        if (!mbar_wait_warp(&sh.tail[slot], phase >> slot & 1, &sh.abort)) return;
+        phase ^= 1u << slot;
+        uint8_t *dst = sKV + slot * C::kTileBytes + valid * 128;
+        const int words = (kBlockN - valid) * 8;
+        for (int b = 0; b < C::kBoxes; ++b)
+            for (int i = lane; i < words; i += 32)
+                *reinterpret_cast<uint4 *>(dst + b * C::kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
+    }
+}
+
+// ------------------------------------------------------------ MMA issuer
+template <int D, bool PAGED>
+__device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_t *sQ, uint8_t *sKV) {
+    using C = Cfg<D>;
+    volatile int *abort = &sh.abort;
+    const uint32_t tmem = sh.tmem_base;
+    const uint32_t idS = idesc_bf16_f32(kBlockM, kBlockN, false);
+    const uint32_t idPV = idesc_bf16_f32(kBlockM, D, true);
+    const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(sKV), 16);
+    const uint32_t v_lo = desc_lo(smem_u32(sKV), C::kBoxBytes);
+    constexpr uint32_t kTileStep = C::kTileBytes >> 4;
+    uint32_t q_uses[2] = {0, 0}, p_cnt[2] = {0, 0}, oe_uses[2] = {0, 0};
+    uint32_t it = 0;
+    // S_t = Q_t K^T (K-major operands, 128-byte swizzle, 64 columns per box)
+    auto issue_s = [&](int t, int slot) {
+        #pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+            mma_ss_lo(tmem + t * kBlockN, q_lo + t * kTileStep + off, k_lo + slot * kTileStep + off,
+                      idS, ks > 0 ? 1u : 0u);
+        }
+        tc_commit(&sh.s_full[t]);
+    };
+    // O_t += P_t V, keys 0-63 when they are there, then 64-127
+    auto issue_pv = [&](int t, int slot, bool &first) -> bool {
+        if (!mbar_wait(&sh.p_lo[t], p_cnt[t] & 1, abort)) return false;
+        if (first) {
+            if (!mbar_wait(&sh.o_empty[t], (oe_uses[t] & 1) ^ 1, abort)) return false;
+            ++oe_uses[t];
+        }
+        #pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half && !mbar_wait(&sh.p_hi[t], p_cnt[t] & 1, abort)) return false;
+            tc_fence_after();
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int ks = half * 4 + k;
+                mma_ts_lo(tmem + C::kColO + t * D, tmem + t * kBlockN + half * 64 + k * 8,
+                          v_lo + slot * kTileStep + ((ks * 2048) >> 4), idPV,
+                          (ks > 0 || !first) ? 1u : 0u);
+            }
+        }
+        ++p_cnt[t];
+        first = false;
+        tc_commit(&sh.o_full[t]);
+        return true;
+    };
+    Walker walk;
+    walk.begin(p, tab);
+    Work w;
+    while (walk.next<PAGED>(p, tab, w)) {
+        const int nb = w.kb1 - w.kb0;
+        bool first[2] = {true, true};
+        for (int t = 0; t < 2; ++t) {
+            if (t == 1 && !w.pair && nb == 1) continue;
+            if (!mbar_wait(&sh.q_full[t], q_uses[t] & 1, abort)) goto out;
+            ++q_uses[t];
+        }
+        int prev_v = -1;
+        uint32_t prev_use = 0;
+        for (int j = 0; j < nb; ++j) {
+            const int ks = it % C::kStages, vs = (it + 1) % C::kStages;
+            if (!mbar_wait(&sh.kv_full[ks], (it / C::kStages) & 1, abort)) goto out;
+            tc_fence_after();
+            const uint32_t v_use = (it + 1) / C::kStages;
+            it += 2;
+            if (w.pair) {
+                issue_s(0, ks);
+                if (j > 0) {
+                    if (!issue_pv(1, prev_v, first[1])) goto out;
+                    tc_commit(&sh.kv_empty[prev_v]);
+                }
+                issue_s(1, ks);
+                tc_commit(&sh.kv_empty[ks]);
+                if (!mbar_wait(&sh.kv_full[vs], v_use & 1, abort)) goto out;
+                tc_fence_after();
+                if (!issue_pv(0, vs, first[0])) goto out;
+            } else {
+                const int t = j & 1;
+                issue_s(t, ks);
+                tc_commit(&sh.kv_empty[ks]);
+                if (j > 0) {
+                    if (!mbar_wait(&sh.kv_full[prev_v], prev_use & 1, abort)) goto out;
+                    tc_fence_after();
+                    if (!issue_pv(t ^ 1, prev_v, first[t ^ 1])) goto out;
+                    tc_commit(&sh.kv_empty[prev_v]);
+                }
+            }
+            prev_v = vs;
+            prev_use = v_use;
+        }
+        const int t = w.pair ? 1 : (nb - 1) & 1;
+        if (!w.pair) {
+            if (!mbar_wait(&sh.kv_full[prev_v], prev_use & 1, abort)) goto out;
+            tc_fence_after();
+        }
+        if (!issue_pv(t, prev_v, first[t])) goto out;
+        tc_commit(&sh.kv_empty[prev_v]);
+    }
+out:
+    // Wait for every MMA this thread issued before TMEM is released.
+    tc_commit(&sh.drain);
+    mbar_drain_wait(&sh.drain, 0);
+}
+
+// ---------------------------------------------------------------- softmax
+template <int NC>
+__device__ __forceinline__ float max_of(const float (&v)[NC]) {
+    float m[4] = {v[0], v[1], v[2], v[3]};
+    #pragma unroll
+    for (int i = 4; i + 7 < NC; i += 8) {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = fmax3(m[e], v[i + e], v[i + 4 + e]);
+    }
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], v[NC - 4 + e]);
+    return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
+}
+
+// P = 2^(s*scale*log2e - m), packed to bf16 pairs (rounded to nearest: off by
+// at most 2^-8 relative, as in the prefill), and their fp32 sum.
+template <int NC>
+__device__ __forceinline__ float exp_of(const float (&v)[NC], float sl2, float m,
+                                        uint32_t (&pk)[NC / 2]) {
+    const uint64_t c2 = f2pack(sl2, sl2), nm2 = f2pack(-m, -m);
+    uint64_t a2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+    #pragma unroll
+    for (int c = 0; c < NC / 2; ++c) {
+        float x0, x1;
+        f2unpack(f2fma(f2pack(v[2 * c], v[2 * c + 1]), c2, nm2), x0, x1);
+        x0 = ex2(x0);
+        x1 = ex2(x1);
+        a2[c & 1] = f2add(a2[c & 1], f2pack(x0, x1));
+        pk[c] = pack_bf16(x0, x1);
+    }
+    float a, b;
+    f2unpack(f2add(a2[0], a2[1]), a, b);
+    return a + b;
+}
+
+// A thread's running softmax: reference maximum (log2 units) and sum.
+struct Row {
+    float m, l;
+};
+
+// Raises the reference maximum if a row of the warp outgrew it by more than
+// the threshold, and rescales O and l with it.  False: a wait ran out.
+template <int D>
+__device__ __forceinline__ bool update_max(Row &r, float m_blk, bool first, uint32_t tO, Shared &sh,
+                                           int t, uint32_t pv_cnt) {
+    if (first) {
+        r.m = m_blk;
+        return true;
+    }
+    if (!__any_sync(0xffffffffu, m_blk > r.m + kRescaleThreshold)) return true;
+    const float m_new = fmaxf(r.m, m_blk);
+    const float alpha = (m_new == -INFINITY) ? 1.f : ex2(r.m - m_new);
+    // O_t holds P V of the block before only once that product is done
+    if (!mbar_wait_warp(&sh.o_full[t], (pv_cnt - 1) & 1, &sh.abort)) return false;
+    tc_fence_after();
+    #pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+        uint32_t ov[16];
+        tmem_ld16(tO + c, ov);
+        tmem_wait_ld();
+        #pragma unroll
+        for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+        tmem_st16(tO + c, ov);
+    }
+    tmem_wait_st();
+    r.l *= alpha;
+    r.m = m_new;
+    return true;
+}
+
+// Keys [col0, col0 + NC) of the block of which `limit` keys are the item's.
+template <int D, int NC>
+__device__ __forceinline__ bool soft_part(Row &r, int col0, int limit, bool first, float sl2,
+                                          uint32_t tS, uint32_t tO, Shared &sh, int t,
+                                          uint32_t pv_cnt, uint32_t (&pk)[NC / 2]) {
+    float s[NC];
+    {
+        uint32_t raw[NC];
+        #pragma unroll
+        for (int c = 0; c < NC; c += 32) tmem_ld32(tS + col0 + c, raw + c);
+        tmem_wait_ld();
+        #pragma unroll
+        for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(raw[c]);
+    }
+    if (limit < kBlockN) {
+        #pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (col0 + c >= limit) s[c] = -INFINITY;
+    }
+    if (!update_max<D>(r, max_of(s) * sl2, first, tO, sh, t, pv_cnt)) return false;
+    r.l += exp_of(s, sl2, r.m == -INFINITY ? 0.f : r.m, pk);
+    return true;
+}
+
+// The softmax of one block, by one warp.  P_t goes over S_t: keys 0-63 in
+// columns 0-31, keys 64-127 in columns 64-95.
+template <int D>
+__device__ __forceinline__ bool soft_block(Row &r, int rep, int limit, bool first, float sl2,
+                                           uint32_t tS, uint32_t tO, Shared &sh, int t,
+                                           uint32_t pv_cnt) {
+    const int q4 = warp_id() & 3;
+    if (rep == 4) {
+        uint32_t pk[16], z[32];
+        if (!soft_part<D, 32>(r, q4 * 32, limit, first, sl2, tS, tO, sh, t, pv_cnt, pk)) return false;
+        #pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0u;
+        const uint32_t half = tS + (q4 >> 1) * 64;
+        tmem_st32(tS + (1 - (q4 >> 1)) * 64, z);
+        tmem_st16(half + (q4 & 1) * 16, pk);
+        tmem_st16(half + (1 - (q4 & 1)) * 16, z);
+    } else if (rep == 2) {
+        uint32_t pk[32], z[32];
+        if (!soft_part<D, 64>(r, (q4 >> 1) * 64, limit, first, sl2, tS, tO, sh, t, pv_cnt, pk))
+            return false;
+        #pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0u;
+        tmem_st32(tS + (q4 >> 1) * 64, pk);
+        tmem_st32(tS + (1 - (q4 >> 1)) * 64, z);
+    } else {
+        float sA[64], sB[64];
+        {
+            uint32_t raw[64];
+            tmem_ld32(tS, raw);
+            tmem_ld32(tS + 32, raw + 32);
+            tmem_wait_ld();
+            #pragma unroll
+            for (int c = 0; c < 64; ++c) sA[c] = __uint_as_float(raw[c]);
+        }
+        uint32_t raw[64];
+        tmem_ld32(tS + 64, raw);
+        tmem_ld32(tS + 96, raw + 32);
+        if (limit < kBlockN) {
+            #pragma unroll
+            for (int c = 0; c < 64; ++c)
+                if (c >= limit) sA[c] = -INFINITY;
+        }
+        const float mA = max_of(sA);
+        tmem_wait_ld();
+        #pragma unroll
+        for (int c = 0; c < 64; ++c) sB[c] = (limit < kBlockN && c + 64 >= limit)
+                                                 ? -INFINITY : __uint_as_float(raw[c]);
+        if (!update_max<D>(r, fmaxf(mA, max_of(sB)) * sl2, first, tO, sh, t, pv_cnt)) return false;
+        const float mb = r.m == -INFINITY ? 0.f : r.m;
+        uint32_t pk[32];
+        r.l += exp_of(sA, sl2, mb, pk);
+        tmem_st32(tS, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane_id() == 0) mbar_arrive(&sh.p_lo[t]);
+        r.l += exp_of(sB, sl2, mb, pk);
+        tmem_st32(tS + 64, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane_id() == 0) mbar_arrive(&sh.p_hi[t]);
+        return true;
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) {
+        mbar_arrive(&sh.p_lo[t]);
+        mbar_arrive(&sh.p_hi[t]);
+    }
+    return true;
+}
+
+template <int D, bool PAGED>
+__device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_t *sQ) {
+    using C = Cfg<D>;
+    const int warp = warp_id(), lane = lane_id(), q4 = warp & 3;
+    const int t = warp >> 2;                  // tile of this warpgroup
+    const int r = q4 * 32 + lane;             // lane of the tile
+    const int kvh = blockIdx.x % p.Hkv;
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tS = sh.tmem_base + lanes + t * kBlockN;
+    const uint32_t tO = sh.tmem_base + lanes + C::kColO + t * D;
+    float *part_o = p.part_o + (size_t)kvh * p.cap * D;
+    float *part_lse = p.part_lse + (size_t)kvh * p.cap;
+    uint32_t s_cnt = 0, pv_cnt = 0;
+    Walker walk;
+    walk.begin(p, tab);
+    Work w;
+    while (walk.next<PAGED>(p, tab, w)) {
+        const int nb = w.kb1 - w.kb0;
+        const int step = w.pair ? 1 : 2;
+        const int j0 = w.kb0 + (w.pair ? 0 : t);
+        const bool used = j0 < w.kb1;
+        const int tile0 = w.pair ? t * kBlockM : 0;       // the tile's first row of the item
+        const int nrows = min(kBlockM, w.it.rows - tile0);
+        const int copy = kBlockM / w.rep;                 // lanes per copy of the rows
+        const int lr = r & (copy - 1);                    // this thread's row of the tile
+        const bool work = (q4 * 32 & (copy - 1)) < nrows; // some lane of the warp has a row
+        bool ok = true;
+        if (used) {
+            // The tile's Q rows, swizzled as TMA would write them.
+            uint4 qv[D / 8];
+            const int row = w.it.row0 + tile0 + lr;
+            if (lr < nrows) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    p.q + ((size_t)(w.it.tok0 + row / p.G) * p.Hq + kvh * p.G + row % p.G) * D);
+                #pragma unroll
+                for (int c = 0; c < D / 8; ++c) qv[c] = __ldg(src + c);
+            } else {
+                #pragma unroll
+                for (int c = 0; c < D / 8; ++c) qv[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            uint8_t *dst = sQ + t * C::kTileBytes + r * 128;
+            #pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBoxBytes + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full[t]);
+        }
+        Row row{-INFINITY, 0.f};
+        for (int j = j0; j < w.kb1 && ok; j += step) {
+            ok = mbar_wait_warp(&sh.s_full[t], s_cnt & 1, &sh.abort);
+            if (!ok) break;
+            ++s_cnt;
+            tc_fence_after();
+            if (work) {
+                ok = soft_block<D>(row, w.rep, w.it.keys - j * kBlockN, j == j0, p.scale_log2, tS, tO,
+                                   sh, t, pv_cnt);
+            } else {
+                // no row in these lanes: what P holds there reaches no other lane
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.p_lo[t]);
+                    mbar_arrive(&sh.p_hi[t]);
+                }
+            }
+            ++pv_cnt;
+        }
+        if (ok && used) {
+            ok = mbar_wait_warp(&sh.o_full[t], (pv_cnt - 1) & 1, &sh.abort);
+            tc_fence_after();
+        }
+        if (w.pair) {
+            // each row has one thread
+            if (ok && work) {
+                const float inv = row.l > 0.f ? 1.f / row.l : 0.f;
+                const size_t at = (size_t)w.slot + tile0 + lr;
+                #pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t ov[32];
+                    tmem_ld32(tO + c, ov);
+                    tmem_wait_ld();
+                    if (lr < nrows) {
+                        float4 *dst = reinterpret_cast<float4 *>(part_o + at * D + c);
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(__uint_as_float(ov[4 * e]) * inv,
+                                                 __uint_as_float(ov[4 * e + 1]) * inv,
+                                                 __uint_as_float(ov[4 * e + 2]) * inv,
+                                                 __uint_as_float(ov[4 * e + 3]) * inv);
+                    }
+                }
+                if (lr < nrows) part_lse[at] = row.l > 0.f ? row.m + __log2f(row.l) : -INFINITY;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_empty[t]);
+            // the warps leave the loop together, or a later barrier would not fill
+            if (!named_bar_and(1, 256, ok)) break;
+            continue;
+        }
+        // Both warpgroups, and the copies of the rows, hold parts of the same
+        // rows: join them.  Q's tiles are free now (every S is done) and hold
+        // the exchange.
+        sh.ml[warp][lane] = make_float2(row.m, row.l);
+        if (!named_bar_and(1, 256, ok)) break;
+        const int quarters = 4 / w.rep;       // warps that hold different rows
+        const int mine = q4 % quarters;
+        float M = -INFINITY, L = 0.f;
+        for (int i = mine; i < 8; i += quarters) M = fmaxf(M, sh.ml[i][lane].x);
+        if (M != -INFINITY)
+            for (int i = mine; i < 8; i += quarters)
+                L += sh.ml[i][lane].y * ex2(sh.ml[i][lane].x - M);
+        const float f = row.l > 0.f && L > 0.f ? ex2(row.m - M) / L : 0.f;
+        if (t == 0 && q4 < quarters && r < nrows)
+            part_lse[(size_t)w.slot + r] = L > 0.f ? M + __log2f(L) : -INFINITY;
+        float *buf = reinterpret_cast<float *>(sQ);
+        constexpr int kLd = C::kChunk + 1;
+        static_assert(8 * 32 * kLd * 4 <= 2 * C::kTileBytes, "exchange within Q's tiles");
+        for (int c0 = 0; c0 < D; c0 += C::kChunk) {
+            float *dst = buf + (warp * 32 + lane) * kLd;
+            if (used && work) {
+                uint32_t ov[C::kChunk];
+                #pragma unroll
+                for (int c = 0; c < C::kChunk; c += 16) tmem_ld16(tO + c0 + c, ov + c);
+                tmem_wait_ld();
+                #pragma unroll
+                for (int e = 0; e < C::kChunk; ++e)
+                    dst[e] = f > 0.f ? __uint_as_float(ov[e]) * f : 0.f;
+            } else {
+                #pragma unroll
+                for (int e = 0; e < C::kChunk; ++e) dst[e] = 0.f;
+            }
+            if (c0 + C::kChunk >= D && used) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.o_empty[t]);
+            }
+            named_bar_sync(1, 256);
+            for (int i = threadIdx.x; i < nrows * C::kChunk; i += 256) {
+                const int rr = i / C::kChunk, c = i % C::kChunk;
+                float sum = 0.f;
+                for (int k = rr >> 5; k < 8; k += quarters) sum += buf[(k * 32 + (rr & 31)) * kLd + c];
+                part_o[((size_t)w.slot + rr) * D + c0 + c] = sum;
+            }
+            named_bar_sync(1, 256);
+        }
+    }
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+              const Params p) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *sKV = smem + C::kOffKV;
+    Table &tab = *reinterpret_cast<Table *>(smem + C::kOffTable);
+    const int warp = warp_id();
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.q_full[t], 4);
+            mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.p_lo[t], 4);
+            mbar_init(&sh.p_hi[t], 4);
+            mbar_init(&sh.o_full[t], 1);
+            mbar_init(&sh.o_empty[t], 4);
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&sh.kv_full[s], 1);
+            mbar_init(&sh.kv_empty[s], 1);
+            mbar_init(&sh.tail[s], 1);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) tmem_alloc(&sh.tmem_base, kTmemCols);
+    if (warp == kWarpTma && lane_id() == 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    make_plan<PAGED>(p, tab, reinterpret_cast<int *>(smem), sh.scan);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 8) {
+        regs_increase<kRegsSoftmax>();
+        softmax_wg<D, PAGED>(p, tab, sh, smem);
+    } else {
+        regs_decrease<kRegsControl>();
+        if (warp == kWarpTma)
+            producer<D, PAGED>(&tmK, &tmV, p, tab, sh, sKV);
+        else if (warp == kWarpClear)
+            clear_tails<D, PAGED>(p, tab, sh, sKV);
+        else if (warp == kWarpMma && lane_id() == 0)
+            mma_issuer<D, PAGED>(p, tab, sh, smem, sKV);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem_base, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- combine
+// One warp per (token, query head): the partials of the row's items.
+constexpr int kCombineWarps = 8;
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(32 * kCombineWarps)
+shared_combine_kernel(const Params p, uint16_t *__restrict__ o, float *__restrict__ lse,
+                      const float *__restrict__ sinks, int tokens) {
+    constexpr int PER = D / 32;
+    const int lane = lane_id();
+    const long long at = (long long)blockIdx.x * kCombineWarps + warp_id();
+    if (at >= (long long)tokens * p.Hq) return;
+    const int tok = (int)(at / p.Hq), h = (int)(at % p.Hq), kvh = h / p.G;
+    // up to two runs of partials: first row, number, rows apart
+    int base[2] = {0, 0}, num[2] = {0, 0}, apart[2] = {0, 0};
+    auto take = [&](int k, int item, int row) {
+        const int4 t = __ldg(p.items + item);
+        base[k] = t.x + row;
+        num[k] = t.y;
+        apart[k] = t.z;
+    };
+    if constexpr (PAGED) {
+        const int4 s = __ldg(p.seqs + tok);
+        take(0, s.x, h % p.G);
+        if (s.y >= 0) {
+            const int row = (tok - s.z) * p.G + h % p.G;
+            take(1, s.y + row / kRows, row % kRows);
+        }
+    } else {
+        const int row = (tok % p.Nq) * p.G + h % p.G;
+        take(0, tok / p.Nq * p.pairs + row / kRows, row % kRows);
+    }
+    const float *po = p.part_o + (size_t)kvh * p.cap * D + lane * PER;
+    const float *pl = p.part_lse + (size_t)kvh * p.cap;
+    const int n = num[0] + num[1];
+    auto row_of = [&](int i) -> size_t {
+        return i < num[0] ? (size_t)base[0] + (size_t)i * apart[0]
+                          : (size_t)base[1] + (size_t)(i - num[0]) * apart[1];
+    };
+    const float z = sinks ? __ldg(sinks + h) * 1.4426950408889634f : -INFINITY;
+    float m = z;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldg(pl + row_of(i)));
+    #pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float acc[PER], sum = 0.f;
+    #pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    if (m != -INFINITY) {
+        sum = ex2(z - m);
+        #pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const size_t rr = row_of(i);
+            const float wgt = ex2(__ldg(pl + rr) - m);
+            sum += wgt;
+            if constexpr (PER == 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(po + rr * D));
+                acc[0] = fmaf(wgt, v.x, acc[0]);
+                acc[1] = fmaf(wgt, v.y, acc[1]);
+                acc[2] = fmaf(wgt, v.z, acc[2]);
+                acc[3] = fmaf(wgt, v.w, acc[3]);
+            } else {
+                const float2 v = __ldg(reinterpret_cast<const float2 *>(po + rr * D));
+                acc[0] = fmaf(wgt, v.x, acc[0]);
+                acc[1] = fmaf(wgt, v.y, acc[1]);
+            }
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(o + ((size_t)tok * p.Hq + h) * D + lane * PER);
+    #pragma unroll
+    for (int e = 0; e < PER; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (lse && lane == 0) {
+        const float v = sum > 0.f ? (m + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        if (PAGED)
+            lse[(size_t)tok * p.Hq + h] = v;
+        else
+            lse[((size_t)(tok / p.Nq) * p.Hq + h) * p.Nq + tok % p.Nq] = v;
+    }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// CTAs per KV head at most; the workspace is sized for them.
+int max_shares(int Hkv) { return Hkv >= kSharedMaxCtas ? 1 : kSharedMaxCtas / Hkv; }
+
+// Rows of partials per KV head.  An item gives one per share it touches: all
+// rows once, and those of the item at each border between shares once more.
+long long part_rows(long long rows, int Hkv, bool twice) {
+    return (twice ? 2 : 1) * rows + (long long)max_shares(Hkv) * (rows < kRows ? rows : kRows);
+}
+
+struct Workspace {
+    size_t o, lse, items, seqs, bytes;
+};
+
+Workspace layout(long long rows, int Hkv, int d, bool paged) {
+    const size_t n = (size_t)part_rows(rows, Hkv, paged) * Hkv;
+    Workspace w;
+    w.o = 0;
+    w.lse = up256(n * d * sizeof(float));
+    w.items = w.lse + up256(n * sizeof(float));
+    w.seqs = w.items + kMaxItems * sizeof(int4);
+    w.bytes = w.seqs + kMaxSeqs * sizeof(int4);
+    return w;
+}
+
+template <int D, bool PAGED>
+int launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, const SharedArgs &a,
+           cudaStream_t stream) {
+    using C = Cfg<D>;
+    constexpr int smem = C::kOffTable + (int)sizeof(Table) + 1024;
+    static_assert(smem + sizeof(Shared) <= 232448, "shared memory");
+    if (cudaFuncSetAttribute(shared_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess)
+        return -5;
+    shared_kernel<D, PAGED><<<p.n * p.Hkv, kThreads, smem, stream>>>(tk, tv, p);
+    if (cudaGetLastError() != cudaSuccess) return -5;
+    const int tokens = p.S * p.Nq;
+    const long long rows = (long long)tokens * p.Hq;
+    shared_combine_kernel<D, PAGED>
+        <<<(unsigned)((rows + kCombineWarps - 1) / kCombineWarps), 32 * kCombineWarps, 0, stream>>>(
+            p, static_cast<uint16_t *>(a.o), a.lse, a.sinks, tokens);
+    return cudaGetLastError() == cudaSuccess ? 0 : -5;
+}
+
+int launch_any(const SharedArgs &a, cudaStream_t stream) {
+    if (a.S <= 0 || a.Nq <= 0) return 0;
+    const int G = a.Hq / a.Hkv;
+    const long long rows = (long long)a.S * a.Nq * G;
+    const Workspace ws = layout(rows, a.Hkv, a.d, a.paged);
+    if (!a.workspace || a.workspace_bytes < ws.bytes) return -4;
+    Params p{};
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.block_table = a.block_table;
+    p.lens = a.lens;
+    p.cu_groups = a.cu_groups;
+    p.prefix_lens = a.prefix_lens;
+    char *base = static_cast<char *>(a.workspace);
+    p.part_o = reinterpret_cast<float *>(base + ws.o);
+    p.part_lse = reinterpret_cast<float *>(base + ws.lse);
+    p.items = reinterpret_cast<int4 *>(base + ws.items);
+    p.seqs = reinterpret_cast<int4 *>(base + ws.seqs);
+    p.S = a.S;
+    p.num_groups = a.num_groups;
+    p.num_pages = a.num_pages;
+    p.max_pages = a.max_pages;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = G;
+    p.Nq = a.Nq;
+    p.Nk = a.Nk;
+    p.pairs = (a.Nq * G + kRows - 1) / kRows;
+    const int sms = device_sm_count() < kSharedMaxCtas ? device_sm_count() : kSharedMaxCtas;
+    p.n = a.Hkv >= sms ? 1 : sms / a.Hkv;
+    p.total_k = a.paged ? 0 : a.S_all * a.Nk;
+    p.cap = part_rows(rows, a.Hkv, a.paged);
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    // K/V rows: the cache's slots, read a page box at a time, or the sequences' stored keys
+    alignas(64) CUtensorMap tk, tv;
+    const bool none = !a.paged && p.total_k == 0;   // no key at all: the maps are not used
+    const void *k = none ? a.q : a.k, *v = none ? a.q : a.v;
+    const uint64_t TK = none ? 1 : a.paged ? (uint64_t)a.num_pages * kPage : (uint64_t)p.total_k;
+    const uint64_t s1 = (uint64_t)a.d * 2, s2 = (uint64_t)a.Hkv * a.d * 2;
+    const uint32_t box = a.paged ? kPage : kBlockN;
+    if (encode_tensor_map_3d(&tk, k, 2, a.d, a.Hkv, TK, s1, s2, 64, 1, box, 128) ||
+        encode_tensor_map_3d(&tv, v, 2, a.d, a.Hkv, TK, s1, s2, 64, 1, box, 128))
+        return -5;
+    if (a.d == 128)
+        return a.paged ? launch<128, true>(tk, tv, p, a, stream) : launch<128, false>(tk, tv, p, a, stream);
+    if (a.d == 64)
+        return a.paged ? launch<64, true>(tk, tv, p, a, stream) : launch<64, false>(tk, tv, p, a, stream);
+    return -2;
+}
+
+}  // namespace shared_impl
+
+size_t shared_workspace_bytes(long long rows_per_kvh, int Hkv, int d, bool paged) {
+    return shared_impl::layout(rows_per_kvh, Hkv, d, paged).bytes;
+}
+
+int launch_shared(const SharedArgs &a, cudaStream_t stream) {
+    return shared_impl::launch_any(a, stream);
+}
+
+}  // namespace fa

@@ -337,6 +337,60 @@ int fa_decode_paged_sinks(const void *q, const void *k_cache, const void *v_cach
                           void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Decode of a batch whose sequences share prefixes ("Paging and prefix
+ * sharing": several block tables name the same pages).  fa_decode_paged reads
+ * a shared page once for each sequence; here the sequences of a group attend
+ * to the pages that they share together, as one matrix product per KV head,
+ * and each to its own pages behind them; the parts are merged with
+ * log-sum-exp.  The result is fa_decode_paged's.
+ *   cu_groups   [num_groups + 1] int32, device, ascending within
+ *               [0, num_seqs]: group g is the sequences cu_groups[g] ..
+ *               cu_groups[g+1]-1.  Sequences of no group are by themselves.
+ *   prefix_lens [num_groups] int32, device: the group's sequences agree in
+ *               their first prefix_lens[g] / 16 block-table entries (whole
+ *               pages; the rest of a partly shared page is each one's own).
+ *               No more is shared than the group's shortest sequence has.
+ *               The group's first sequence's entries are read for all; 0 is
+ *               always right.
+ *   sinks       [Hq] fp32 learned sink logits, or NULL (as fa_fwd_sinks)
+ *   workspace   fa_decode_shared_workspace_bytes(...) bytes, 256-byte aligned,
+ *               not to be shared by calls that may overlap on the GPU.
+ *   num_seqs at most 1024 and Hq / Hkv at most 128 (else
+ *   FA_ERR_UNSUPPORTED), num_groups at most num_seqs.
+ * Other arguments as for fa_decode_paged.  Device-side errors, reported
+ * through fa_check_device_error as FA_ERR_INVALID_ARG: a length outside
+ * [0, max_pages_per_seq * 16] is clamped, a page outside the cache is read as
+ * page 0, cu_groups that does not ascend within the batch counts as no group,
+ * a negative prefix as 0.
+ */
+size_t fa_decode_shared_workspace_bytes(int num_seqs, int Hq, int Hkv, int d);
+int fa_decode_shared(const void *q, const void *k_cache, const void *v_cache,
+                     const int *block_table, const int *seq_lens, const int *cu_groups,
+                     const int *prefix_lens, void *o, float *lse, const float *sinks, int num_seqs,
+                     int num_groups, int num_pages, int Hq, int Hkv, int d, int page_size,
+                     int max_pages_per_seq, float scale, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * Cross attention of few queries: the decoder's next token (Nq = 1), or the
+ * few of a speculated step, against its encoder states.  fa_fwd_cross's
+ * layouts, result and treatment of rows behind seq_lens_k (which may be NULL),
+ * with o bf16; the keys are split over the whole GPU ("Flash-Decoding"),
+ * where fa_fwd_cross gives each 256 queries of a head to one SM: the better
+ * call while B * Hq * ceil(Nq / 256) is below the number of SMs or Nq * Hq /
+ * Hkv is small.  A length outside [0, Nk] is clamped and reported
+ * (fa_check_device_error, FA_ERR_INVALID_ARG).
+ *   workspace   fa_decode_cross_workspace_bytes(...) bytes, 256-byte aligned,
+ *               not to be shared by calls that may overlap on the GPU.
+ *   Hq / Hkv at most 128, Nq * Hq / Hkv at most 524288 (else
+ *   FA_ERR_UNSUPPORTED).
+ */
+size_t fa_decode_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
+int fa_decode_cross(const void *q, const void *k, const void *v, const int *seq_lens_k, void *o,
+                    float *lse, int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * fa_decode_paged over an FP8 cache ("FP8 KV cache": the post's cache-size
  * paragraphs before "Paging and prefix sharing" -- fewer bits per cached
  * value).  k_cache/v_cache [num_pages, page_size, Hkv, d] hold OCP FP8 E4M3
