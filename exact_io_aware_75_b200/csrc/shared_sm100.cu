@@ -66,6 +66,7 @@ constexpr int kMaxSeqs = kSharedMaxSeqs;    // sequences per launch
 constexpr int kMaxGroupItems = 1024;        // group <= 128 heads: at most S/2 + S/2 items
 constexpr int kMaxItems = kSharedMaxItems;
 static_assert(kMaxSeqs + kMaxGroupItems <= kMaxItems, "items of a paged batch");
+constexpr int kFewRows = 16;                // rows the two warpgroups exchange at once
 // Cost of a key block, in half tiles of K/V read from HBM, and of an item
 // besides (its first loads and its epilogue).
 constexpr int kCostBlock = 2, kCostBlock2 = 3, kCostItem = 1;
@@ -75,7 +76,7 @@ struct Cfg {
     static constexpr int kBoxes = D / 64;
     static constexpr int kBoxBytes = kBlockM * 128;            // 128 rows x 128 bytes
     static constexpr int kTileBytes = kBlockM * D * 2;
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStages = D == 128 ? 4 : 8;           // K in the even slots, V in the odd
     static constexpr int kOffKV = 2 * kTileBytes;
     static constexpr int kOffTable = kOffKV + kStages * kTileBytes;
     static constexpr uint32_t kColO = 256;                     // O_t at 256 + t*D
@@ -84,10 +85,12 @@ struct Cfg {
 
 // The plan, in shared memory.
 struct Table {
-    int start[kMaxItems];      // cost before the item
-    int slot[kMaxItems];       // partial rows before the item
-    int2 gi[kMaxGroupItems];   // group items: first sequence | count << 16, pages | row pair << 22
-    int own[kMaxSeqs];         // pages of each sequence that its group reads
+    int start[kMaxItems];            // cost before the item
+    int slot[kMaxItems];             // partial rows before the item
+    uint32_t gi[kMaxGroupItems];     // group items: group | row pair << 16
+    uint16_t cu[kMaxSeqs + 2];       // first sequence of each group
+    int own[kMaxSeqs];               // pages of each sequence that its group reads
+    int keys[kMaxSeqs];              // keys behind them (not paged: all keys)
     int num_group_items, num_items, span;
 };
 
@@ -99,6 +102,7 @@ struct Params {
     int4 *seqs;                // {own item, first group item or -1, group's first sequence, -}
     int S, num_groups, num_pages, max_pages;
     int Hq, Hkv, G, Nq, Nk, pairs;
+    uint32_t G_magic;
     int n;                     // CTAs per KV head
     int total_k;               // dense: stored key rows
     long long cap;
@@ -118,12 +122,12 @@ struct Shared {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// A sequence's length, clamped to what its table (or its stored keys) can hold.
 template <bool PAGED>
-__device__ __forceinline__ int length_of(const Params &p, int s, bool report) {
+__device__ __forceinline__ int good_length(const Params &p, int L) {
     const int most = PAGED ? p.max_pages * kPage : p.Nk;
-    int L = p.lens ? __ldg(p.lens + s) : most;
     if (L < 0 || L > most) {
-        if (report) report_error(kDevErrInput);
+        if (blockIdx.x == 0) report_error(kDevErrInput);
         L = L < 0 ? 0 : most;
     }
     return L;
@@ -146,25 +150,36 @@ __device__ __forceinline__ Item get_item(const Params &p, const Table &tab, int 
     w.page0 = 0;
     if constexpr (PAGED) {
         if (i < tab.num_group_items) {
-            const int2 g = tab.gi[i];
-            w.tok0 = w.src = g.x & 0xffff;
-            all = (g.x >> 16) * p.G;
-            w.row0 = (g.y >> 22) * kRows;
-            w.keys = (g.y & 0x3fffff) * kPage;
+            const int g = tab.gi[i] & 0xffff, first = tab.cu[g];
+            w.tok0 = w.src = first;
+            all = (tab.cu[g + 1] - first) * p.G;
+            w.row0 = (int)(tab.gi[i] >> 16) * kRows;
+            w.keys = tab.own[first] * kPage;
         } else {
             w.tok0 = w.src = i - tab.num_group_items;
             w.page0 = tab.own[w.src];
-            w.keys = max(0, length_of<true>(p, w.src, false) - w.page0 * kPage);
+            w.keys = tab.keys[w.src];
         }
     } else {
-        w.src = i / p.pairs;
+        w.src = p.pairs == 1 ? i : i / p.pairs;
         w.tok0 = w.src * p.Nq;
-        w.row0 = (i % p.pairs) * kRows;
-        w.keys = length_of<false>(p, w.src, false);
+        w.row0 = (i - w.src * p.pairs) * kRows;
+        w.keys = tab.keys[w.src];
     }
     w.rows = min(kRows, all - w.row0);
     return w;
 }
+
+// x / G for the rows of a launch (G_magic = ceil(2^32 / G), exact as x * G < 2^32).
+__device__ __forceinline__ int div_group(const Params &p, int x) {
+    return p.G == 1 ? x : (int)__umulhi((uint32_t)x, p.G_magic);
+}
+
+// ceil(x / cost) for the two costs, x < 2^30.
+__device__ __forceinline__ int div_cost(int x, int cost) {
+    return cost == kCostBlock ? (x + 1) >> 1 : (int)__umulhi((uint32_t)(x + 2), 0x55555556u);
+}
+static_assert(kCostBlock == 2 && kCostBlock2 == 3, "div_cost");
 
 __device__ __forceinline__ int block_cost(int rows) { return rows > kBlockM ? kCostBlock2 : kCostBlock; }
 
@@ -191,19 +206,28 @@ __device__ __forceinline__ int block_scan(int x, int *s_warp, int &total) {
 }
 
 // All threads of the block; ends with a barrier.  `scratch`: room for
-// 3 * kMaxSeqs + 1 ints.
+// 3 * kMaxSeqs + 1 ints.  Everything read from global memory is asked for at
+// once, so that the plan costs one latency and some barriers.
 template <bool PAGED>
 __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp) {
     const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
-    int ni = 0;
-    if constexpr (PAGED) {
-        int *cu = scratch, *pages = cu + kMaxSeqs + 1, *first = pages + kMaxSeqs;
-        int ng = p.num_groups;
+    int ni = 0, ng = PAGED ? p.num_groups : 0;
+    int *cu = scratch, *least = cu + kMaxSeqs + 1, *prefix = least + kMaxSeqs;
+    if (PAGED && ng > 0) {
         for (int g = tid; g <= ng; g += kThreads) {
-            if (ng > 0) cu[g] = __ldg(p.cu_groups + g);
-            if (g < ng) pages[g] = INT_MAX;
+            cu[g] = __ldg(p.cu_groups + g);
+            if (g < ng) {
+                prefix[g] = __ldg(p.prefix_lens + g);
+                least[g] = INT_MAX;
+            }
         }
+    }
+    for (int s = tid; s < p.S; s += kThreads) {
+        tab.keys[s] = good_length<PAGED>(p, p.lens ? __ldg(p.lens + s) : p.Nk);
+        tab.own[s] = 0;
+    }
+    if (PAGED && ng > 0) {
         __syncthreads();
         bool bad = false;
         for (int g = tid; g < ng; g += kThreads)
@@ -222,39 +246,43 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
         };
         // no more is shared than the group's shortest sequence has
         for (int s = tid; s < p.S; s += kThreads) {
-            const int g = group_of(s), L = length_of<true>(p, s, lead);
-            if (g >= 0) atomicMin(&pages[g], L);
+            const int g = group_of(s);
+            if (g >= 0) atomicMin(&least[g], tab.keys[s]);
         }
         __syncthreads();
         for (int g0 = 0; g0 < ng; g0 += kThreads) {
             const int g = g0 + tid;
-            int cnt = 0, pg = 0, items = 0;
+            int items = 0, pages = 0;
             if (g < ng) {
-                int len = __ldg(p.prefix_lens + g);
+                int len = prefix[g];
                 if (len < 0) {
                     if (lead) report_error(kDevErrInput);
                     len = 0;
                 }
-                cnt = cu[g + 1] - cu[g];
-                pg = cnt >= 2 ? min(len, pages[g]) / kPage : 0;
-                items = pg > 0 ? ceil_div(cnt * p.G, kRows) : 0;
+                const int cnt = cu[g + 1] - cu[g];
+                if (cnt >= 2) pages = min(len, least[g]) / kPage;
+                if (pages > 0) items = ceil_div(cnt * p.G, kRows);
             }
             int total;
             const int base = ni + block_scan(items, s_warp, total);
             ni += total;
             if (g < ng) {
-                pages[g] = pg;
-                first[g] = pg > 0 ? base : -1;
-                for (int r = 0; r < items; ++r)
-                    tab.gi[base + r] = make_int2(cu[g] | cnt << 16, pg | r << 22);
+                least[g] = pages;
+                prefix[g] = pages > 0 ? base : -1;       // now the group's first item
+                tab.cu[g] = (uint16_t)cu[g];
+                if (g == ng - 1) tab.cu[ng] = (uint16_t)cu[ng];
+                for (int r = 0; r < items; ++r) tab.gi[base + r] = (uint32_t)g | (uint32_t)r << 16;
             }
         }
         __syncthreads();
         for (int s = tid; s < p.S; s += kThreads) {
-            const int g = group_of(s);
-            tab.own[s] = g >= 0 ? pages[g] : 0;
-            if (lead) p.seqs[s] = make_int4(ni + s, g >= 0 ? first[g] : -1, g >= 0 ? cu[g] : 0, 0);
+            const int g = group_of(s), pages = g >= 0 ? least[g] : 0;
+            tab.own[s] = pages;
+            tab.keys[s] -= pages * kPage;
+            if (lead) p.seqs[s] = make_int4(ni + s, g >= 0 ? prefix[g] : -1, g >= 0 ? cu[g] : 0, 0);
         }
+    } else if (PAGED && lead) {
+        for (int s = tid; s < p.S; s += kThreads) p.seqs[s] = make_int4(s, -1, 0, 0);
     }
     const int N = PAGED ? ni + p.S : p.S * p.pairs;
     if (tid == 0) {
@@ -267,7 +295,6 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     int sum = 0, total;
     for (int i = i0; i < i1; ++i) {
         const Item w = get_item<PAGED>(p, tab, i);
-        if (!PAGED && lead && w.row0 == 0) length_of<false>(p, w.src, true);
         tab.start[i] = sum;
         if (w.keys > 0) sum += ceil_div(w.keys, kBlockN) * block_cost(w.rows) + kCostItem;
     }
@@ -311,10 +338,10 @@ struct Work {
 };
 
 struct Walker {
-    int i, lo, hi;
+    int i, lo, hi, share;
     __device__ __forceinline__ void begin(const Params &p, const Table &tab) {
-        const int c = blockIdx.x / p.Hkv;
-        lo = c * tab.span;
+        share = blockIdx.x / p.Hkv;
+        lo = share * tab.span;
         hi = lo + tab.span;
         int a = 0, b = tab.num_items;          // the last item that starts at or before lo
         while (b - a > 1) {
@@ -330,12 +357,12 @@ struct Walker {
             if (start >= hi) return false;
             w.it = get_item<PAGED>(p, tab, i);
             const int cost = block_cost(w.it.rows), nb = ceil_div(w.it.keys, kBlockN);
-            w.kb0 = start >= lo ? 0 : min(nb, ceil_div(lo - start, cost));
-            w.kb1 = min(nb, ceil_div(hi - start, cost));
+            w.kb0 = start >= lo ? 0 : min(nb, div_cost(lo - start, cost));
+            w.kb1 = min(nb, div_cost(hi - start, cost));
             if (w.kb0 >= w.kb1) continue;
             w.pair = w.it.rows > kBlockM;
             w.rep = w.it.rows > 64 ? 1 : w.it.rows > 32 ? 2 : 4;
-            w.slot = tab.slot[i] + (lo / tab.span - start / tab.span) * w.it.rows;
+            w.slot = tab.slot[i] + (start >= lo ? 0 : share - start / tab.span) * w.it.rows;
             ++i;
             return true;
         }
@@ -448,6 +475,11 @@ __device__ void clear_tails(const Params &p, const Table &tab, Shared &sh, uint8
 }
 
 // ------------------------------------------------------------ MMA issuer
+// A whole warp, of which one lane issues.  Commits cost it some 250 cycles
+// each, so a block has two: S's, upon which the softmax warps hand the K slot
+// back, and that of the V slot.  Products complete in the order of their
+// issue, so with S of a tile's next block P V of the block before is done;
+// O's own commit comes after a share's last block.
 template <int D, bool PAGED>
 __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_t *sQ, uint8_t *sKV) {
     using C = Cfg<D>;
@@ -462,36 +494,43 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
     uint32_t it = 0;
     // S_t = Q_t K^T (K-major operands, 128-byte swizzle, 64 columns per box)
     auto issue_s = [&](int t, int slot) {
-        #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
-            mma_ss_lo(tmem + t * kBlockN, q_lo + t * kTileStep + off, k_lo + slot * kTileStep + off,
-                      idS, ks > 0 ? 1u : 0u);
+        if (elect_one()) {
+            #pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+                mma_ss_lo(tmem + t * kBlockN, q_lo + t * kTileStep + off, k_lo + slot * kTileStep + off,
+                          idS, ks > 0 ? 1u : 0u);
+            }
+            tc_commit(&sh.s_full[t]);
         }
-        tc_commit(&sh.s_full[t]);
+        __syncwarp();
     };
     // O_t += P_t V, keys 0-63 when they are there, then 64-127
-    auto issue_pv = [&](int t, int slot, bool &first) -> bool {
-        if (!mbar_wait(&sh.p_lo[t], p_cnt[t] & 1, abort)) return false;
+    auto issue_pv = [&](int t, int slot, bool &first, bool last, bool free) -> bool {
+        if (!mbar_wait_warp(&sh.p_lo[t], p_cnt[t] & 1, abort)) return false;
         if (first) {
-            if (!mbar_wait(&sh.o_empty[t], (oe_uses[t] & 1) ^ 1, abort)) return false;
+            if (!mbar_wait_warp(&sh.o_empty[t], (oe_uses[t] & 1) ^ 1, abort)) return false;
             ++oe_uses[t];
         }
         #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            if (half && !mbar_wait(&sh.p_hi[t], p_cnt[t] & 1, abort)) return false;
+            if (half && !mbar_wait_warp(&sh.p_hi[t], p_cnt[t] & 1, abort)) return false;
             tc_fence_after();
-            #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int ks = half * 4 + k;
-                mma_ts_lo(tmem + C::kColO + t * D, tmem + t * kBlockN + half * 64 + k * 8,
-                          v_lo + slot * kTileStep + ((ks * 2048) >> 4), idPV,
-                          (ks > 0 || !first) ? 1u : 0u);
+            if (elect_one()) {
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int ks = half * 4 + k;
+                    mma_ts_lo(tmem + C::kColO + t * D, tmem + t * kBlockN + half * 64 + k * 8,
+                              v_lo + slot * kTileStep + ((ks * 2048) >> 4), idPV,
+                              (ks > 0 || !first) ? 1u : 0u);
+                }
+                if (half && free) tc_commit(&sh.kv_empty[slot]);
+                if (half && last) tc_commit(&sh.o_full[t]);
             }
+            __syncwarp();
         }
         ++p_cnt[t];
         first = false;
-        tc_commit(&sh.o_full[t]);
         return true;
     };
     Walker walk;
@@ -502,37 +541,33 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
         bool first[2] = {true, true};
         for (int t = 0; t < 2; ++t) {
             if (t == 1 && !w.pair && nb == 1) continue;
-            if (!mbar_wait(&sh.q_full[t], q_uses[t] & 1, abort)) goto out;
+            if (!mbar_wait_warp(&sh.q_full[t], q_uses[t] & 1, abort)) goto out;
             ++q_uses[t];
         }
         int prev_v = -1;
         uint32_t prev_use = 0;
         for (int j = 0; j < nb; ++j) {
             const int ks = it % C::kStages, vs = (it + 1) % C::kStages;
-            if (!mbar_wait(&sh.kv_full[ks], (it / C::kStages) & 1, abort)) goto out;
+            if (!mbar_wait_warp(&sh.kv_full[ks], (it / C::kStages) & 1, abort)) goto out;
             tc_fence_after();
             const uint32_t v_use = (it + 1) / C::kStages;
             it += 2;
             if (w.pair) {
                 issue_s(0, ks);
                 if (j > 0) {
-                    if (!issue_pv(1, prev_v, first[1])) goto out;
-                    tc_commit(&sh.kv_empty[prev_v]);
+                    if (!issue_pv(1, prev_v, first[1], false, true)) goto out;
                 }
                 issue_s(1, ks);
-                tc_commit(&sh.kv_empty[ks]);
-                if (!mbar_wait(&sh.kv_full[vs], v_use & 1, abort)) goto out;
+                if (!mbar_wait_warp(&sh.kv_full[vs], v_use & 1, abort)) goto out;
                 tc_fence_after();
-                if (!issue_pv(0, vs, first[0])) goto out;
+                if (!issue_pv(0, vs, first[0], j == nb - 1, false)) goto out;
             } else {
                 const int t = j & 1;
                 issue_s(t, ks);
-                tc_commit(&sh.kv_empty[ks]);
                 if (j > 0) {
-                    if (!mbar_wait(&sh.kv_full[prev_v], prev_use & 1, abort)) goto out;
+                    if (!mbar_wait_warp(&sh.kv_full[prev_v], prev_use & 1, abort)) goto out;
                     tc_fence_after();
-                    if (!issue_pv(t ^ 1, prev_v, first[t ^ 1])) goto out;
-                    tc_commit(&sh.kv_empty[prev_v]);
+                    if (!issue_pv(t ^ 1, prev_v, first[t ^ 1], j == nb - 1, true)) goto out;
                 }
             }
             prev_v = vs;
@@ -540,15 +575,15 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
         }
         const int t = w.pair ? 1 : (nb - 1) & 1;
         if (!w.pair) {
-            if (!mbar_wait(&sh.kv_full[prev_v], prev_use & 1, abort)) goto out;
+            if (!mbar_wait_warp(&sh.kv_full[prev_v], prev_use & 1, abort)) goto out;
             tc_fence_after();
         }
-        if (!issue_pv(t, prev_v, first[t])) goto out;
-        tc_commit(&sh.kv_empty[prev_v]);
+        if (!issue_pv(t, prev_v, first[t], true, true)) goto out;
     }
 out:
     // Wait for every MMA this thread issued before TMEM is released.
-    tc_commit(&sh.drain);
+    if (elect_one()) tc_commit(&sh.drain);
+    __syncwarp();
     mbar_drain_wait(&sh.drain, 0);
 }
 
@@ -593,20 +628,17 @@ struct Row {
 };
 
 // Raises the reference maximum if a row of the warp outgrew it by more than
-// the threshold, and rescales O and l with it.  False: a wait ran out.
+// the threshold, and rescales O and l with it (P V of the block before is
+// done: its completion came with this block's S).
 template <int D>
-__device__ __forceinline__ bool update_max(Row &r, float m_blk, bool first, uint32_t tO, Shared &sh,
-                                           int t, uint32_t pv_cnt) {
+__device__ __forceinline__ void update_max(Row &r, float m_blk, bool first, uint32_t tO) {
     if (first) {
         r.m = m_blk;
-        return true;
+        return;
     }
-    if (!__any_sync(0xffffffffu, m_blk > r.m + kRescaleThreshold)) return true;
+    if (!__any_sync(0xffffffffu, m_blk > r.m + kRescaleThreshold)) return;
     const float m_new = fmaxf(r.m, m_blk);
     const float alpha = (m_new == -INFINITY) ? 1.f : ex2(r.m - m_new);
-    // O_t holds P V of the block before only once that product is done
-    if (!mbar_wait_warp(&sh.o_full[t], (pv_cnt - 1) & 1, &sh.abort)) return false;
-    tc_fence_after();
     #pragma unroll 1
     for (int c = 0; c < D; c += 16) {
         uint32_t ov[16];
@@ -619,14 +651,12 @@ __device__ __forceinline__ bool update_max(Row &r, float m_blk, bool first, uint
     tmem_wait_st();
     r.l *= alpha;
     r.m = m_new;
-    return true;
 }
 
 // Keys [col0, col0 + NC) of the block of which `limit` keys are the item's.
 template <int D, int NC>
-__device__ __forceinline__ bool soft_part(Row &r, int col0, int limit, bool first, float sl2,
-                                          uint32_t tS, uint32_t tO, Shared &sh, int t,
-                                          uint32_t pv_cnt, uint32_t (&pk)[NC / 2]) {
+__device__ __forceinline__ void soft_part(Row &r, int col0, int limit, bool first, float sl2,
+                                          uint32_t tS, uint32_t tO, uint32_t (&pk)[NC / 2]) {
     float s[NC];
     {
         uint32_t raw[NC];
@@ -641,21 +671,19 @@ __device__ __forceinline__ bool soft_part(Row &r, int col0, int limit, bool firs
         for (int c = 0; c < NC; ++c)
             if (col0 + c >= limit) s[c] = -INFINITY;
     }
-    if (!update_max<D>(r, max_of(s) * sl2, first, tO, sh, t, pv_cnt)) return false;
+    update_max<D>(r, max_of(s) * sl2, first, tO);
     r.l += exp_of(s, sl2, r.m == -INFINITY ? 0.f : r.m, pk);
-    return true;
 }
 
 // The softmax of one block, by one warp.  P_t goes over S_t: keys 0-63 in
 // columns 0-31, keys 64-127 in columns 64-95.
 template <int D>
-__device__ __forceinline__ bool soft_block(Row &r, int rep, int limit, bool first, float sl2,
-                                           uint32_t tS, uint32_t tO, Shared &sh, int t,
-                                           uint32_t pv_cnt) {
+__device__ __forceinline__ void soft_block(Row &r, int rep, int limit, bool first, float sl2,
+                                           uint32_t tS, uint32_t tO, Shared &sh, int t) {
     const int q4 = warp_id() & 3;
     if (rep == 4) {
         uint32_t pk[16], z[32];
-        if (!soft_part<D, 32>(r, q4 * 32, limit, first, sl2, tS, tO, sh, t, pv_cnt, pk)) return false;
+        soft_part<D, 32>(r, q4 * 32, limit, first, sl2, tS, tO, pk);
         #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = 0u;
         const uint32_t half = tS + (q4 >> 1) * 64;
@@ -664,8 +692,7 @@ __device__ __forceinline__ bool soft_block(Row &r, int rep, int limit, bool firs
         tmem_st16(half + (1 - (q4 & 1)) * 16, z);
     } else if (rep == 2) {
         uint32_t pk[32], z[32];
-        if (!soft_part<D, 64>(r, (q4 >> 1) * 64, limit, first, sl2, tS, tO, sh, t, pv_cnt, pk))
-            return false;
+        soft_part<D, 64>(r, (q4 >> 1) * 64, limit, first, sl2, tS, tO, pk);
         #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = 0u;
         tmem_st32(tS + (q4 >> 1) * 64, pk);
@@ -693,22 +720,26 @@ __device__ __forceinline__ bool soft_block(Row &r, int rep, int limit, bool firs
         #pragma unroll
         for (int c = 0; c < 64; ++c) sB[c] = (limit < kBlockN && c + 64 >= limit)
                                                  ? -INFINITY : __uint_as_float(raw[c]);
-        if (!update_max<D>(r, fmaxf(mA, max_of(sB)) * sl2, first, tO, sh, t, pv_cnt)) return false;
+        update_max<D>(r, fmaxf(mA, max_of(sB)) * sl2, first, tO);
         const float mb = r.m == -INFINITY ? 0.f : r.m;
         uint32_t pk[32];
-        r.l += exp_of(sA, sl2, mb, pk);
+        uint64_t acc = f2pack(0.f, 0.f);
+        prefill_impl::exp_half(sA, sl2, mb, pk, acc);
         tmem_st32(tS, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane_id() == 0) mbar_arrive(&sh.p_lo[t]);
-        r.l += exp_of(sB, sl2, mb, pk);
+        prefill_impl::exp_half(sB, sl2, mb, pk, acc);
         tmem_st32(tS + 64, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane_id() == 0) mbar_arrive(&sh.p_hi[t]);
-        return true;
+        float a0, a1;
+        f2unpack(acc, a0, a1);
+        r.l += a0 + a1;
+        return;
     }
     tmem_wait_st();
     tc_fence_before();
@@ -717,7 +748,6 @@ __device__ __forceinline__ bool soft_block(Row &r, int rep, int limit, bool firs
         mbar_arrive(&sh.p_lo[t]);
         mbar_arrive(&sh.p_hi[t]);
     }
-    return true;
 }
 
 template <int D, bool PAGED>
@@ -732,12 +762,30 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
     const uint32_t tO = sh.tmem_base + lanes + C::kColO + t * D;
     float *part_o = p.part_o + (size_t)kvh * p.cap * D;
     float *part_lse = p.part_lse + (size_t)kvh * p.cap;
-    uint32_t s_cnt = 0, pv_cnt = 0;
+    uint32_t s_cnt = 0, o_cnt = 0, it = 0;
+    // This thread's row of a share's Q tile, in registers: asked for while the
+    // share before is joined.
+    uint4 qv[D / 8];
+    auto load_q = [&](const Work &w) {
+        const int tile0 = w.pair ? t * kBlockM : 0;
+        const int lr = r & (kBlockM / w.rep - 1), row = w.it.row0 + tile0 + lr;
+        if (lr < min(kBlockM, w.it.rows - tile0)) {
+            const int tok = div_group(p, row);
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + ((size_t)(w.it.tok0 + tok) * p.Hq + kvh * p.G + row - tok * p.G) * D);
+            #pragma unroll
+            for (int c = 0; c < D / 8; ++c) qv[c] = __ldg(src + c);
+        } else {
+            #pragma unroll
+            for (int c = 0; c < D / 8; ++c) qv[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
     Walker walk;
     walk.begin(p, tab);
-    Work w;
-    while (walk.next<PAGED>(p, tab, w)) {
-        const int nb = w.kb1 - w.kb0;
+    Work w, after;
+    bool have = walk.next<PAGED>(p, tab, w);
+    if (have) load_q(w);
+    for (; have; w = after) {
         const int step = w.pair ? 1 : 2;
         const int j0 = w.kb0 + (w.pair ? 0 : t);
         const bool used = j0 < w.kb1;
@@ -747,19 +795,7 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
         const int lr = r & (copy - 1);                    // this thread's row of the tile
         const bool work = (q4 * 32 & (copy - 1)) < nrows; // some lane of the warp has a row
         bool ok = true;
-        if (used) {
-            // The tile's Q rows, swizzled as TMA would write them.
-            uint4 qv[D / 8];
-            const int row = w.it.row0 + tile0 + lr;
-            if (lr < nrows) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    p.q + ((size_t)(w.it.tok0 + row / p.G) * p.Hq + kvh * p.G + row % p.G) * D);
-                #pragma unroll
-                for (int c = 0; c < D / 8; ++c) qv[c] = __ldg(src + c);
-            } else {
-                #pragma unroll
-                for (int c = 0; c < D / 8; ++c) qv[c] = make_uint4(0u, 0u, 0u, 0u);
-            }
+        if (used) {                                       // swizzled as TMA would write them
             uint8_t *dst = sQ + t * C::kTileBytes + r * 128;
             #pragma unroll
             for (int c = 0; c < D / 8; ++c)
@@ -774,9 +810,12 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
             if (!ok) break;
             ++s_cnt;
             tc_fence_after();
+            // the block's K slot, handed back by two warps: one of each tile
+            // where both read it, else two of this one
+            if (lane == 0 && q4 < (w.pair ? 1 : 2))
+                mbar_arrive(&sh.kv_empty[(it + 2 * (j - w.kb0)) % C::kStages]);
             if (work) {
-                ok = soft_block<D>(row, w.rep, w.it.keys - j * kBlockN, j == j0, p.scale_log2, tS, tO,
-                                   sh, t, pv_cnt);
+                soft_block<D>(row, w.rep, w.it.keys - j * kBlockN, j == j0, p.scale_log2, tS, tO, sh, t);
             } else {
                 // no row in these lanes: what P holds there reaches no other lane
                 tc_fence_before();
@@ -786,12 +825,14 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
                     mbar_arrive(&sh.p_hi[t]);
                 }
             }
-            ++pv_cnt;
         }
+        have = walk.next<PAGED>(p, tab, after);
+        if (have) load_q(after);
         if (ok && used) {
-            ok = mbar_wait_warp(&sh.o_full[t], (pv_cnt - 1) & 1, &sh.abort);
+            ok = mbar_wait_warp(&sh.o_full[t], o_cnt++ & 1, &sh.abort);
             tc_fence_after();
         }
+        it += 2 * (w.kb1 - w.kb0);
         if (w.pair) {
             // each row has one thread
             if (ok && work) {
@@ -827,16 +868,70 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
         sh.ml[warp][lane] = make_float2(row.m, row.l);
         if (!named_bar_and(1, 256, ok)) break;
         const int quarters = 4 / w.rep;       // warps that hold different rows
-        const int mine = q4 % quarters;
+        const int mine = q4 & (quarters - 1);
         float M = -INFINITY, L = 0.f;
-        for (int i = mine; i < 8; i += quarters) M = fmaxf(M, sh.ml[i][lane].x);
-        if (M != -INFINITY)
-            for (int i = mine; i < 8; i += quarters)
-                L += sh.ml[i][lane].y * ex2(sh.ml[i][lane].x - M);
+        float2 part[8];
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            part[i] = sh.ml[i][lane];
+            if ((i & (quarters - 1)) != mine) part[i] = make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, part[i].x);
+        }
+        const float M0 = M == -INFINITY ? 0.f : M;
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) L = fmaf(part[i].y, ex2(part[i].x - M0), L);
         const float f = row.l > 0.f && L > 0.f ? ex2(row.m - M) / L : 0.f;
         if (t == 0 && q4 < quarters && r < nrows)
             part_lse[(size_t)w.slot + r] = L > 0.f ? M + __log2f(L) : -INFINITY;
         float *buf = reinterpret_cast<float *>(sQ);
+        const int warps = w.kb1 - w.kb0 > 1 ? 8 : 4;      // (of one block, the first warpgroup only)
+        if (nrows <= kFewRows) {
+            // Few rows (every warp has all of them in its first lanes): whole
+            // rows at once, 16-byte words turned by the row against conflicts.
+            constexpr int kWords = D / 4;
+            static_assert(8 * kFewRows * D * 4 <= 2 * C::kTileBytes, "exchange within Q's tiles");
+            float4 *b4 = reinterpret_cast<float4 *>(buf);
+            if (used) {
+                #pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    uint32_t ov[64];
+                    tmem_ld32(tO + c0, ov);
+                    tmem_ld32(tO + c0 + 32, ov + 32);
+                    tmem_wait_ld();
+                    if (lane < nrows) {
+                        #pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (f > 0.f)
+                                v = make_float4(__uint_as_float(ov[4 * e]) * f, __uint_as_float(ov[4 * e + 1]) * f,
+                                                __uint_as_float(ov[4 * e + 2]) * f, __uint_as_float(ov[4 * e + 3]) * f);
+                            b4[(warp * kFewRows + lane) * kWords + ((c0 / 4 + e + lane) & (kWords - 1))] = v;
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.o_empty[t]);
+            }
+            named_bar_sync(1, 256);
+            for (int i = threadIdx.x; i < nrows * kWords; i += 256) {
+                const int rr = i / kWords, c = i % kWords;
+                const float4 *src = b4 + rr * kWords + ((c + rr) & (kWords - 1));
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                #pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < warps) {
+                        const float4 v = src[k * kFewRows * kWords];
+                        sum.x += v.x;
+                        sum.y += v.y;
+                        sum.z += v.z;
+                        sum.w += v.w;
+                    }
+                reinterpret_cast<float4 *>(part_o + ((size_t)w.slot + rr) * D)[c] = sum;
+            }
+            named_bar_sync(1, 256);
+            continue;
+        }
         constexpr int kLd = C::kChunk + 1;
         static_assert(8 * 32 * kLd * 4 <= 2 * C::kTileBytes, "exchange within Q's tiles");
         for (int c0 = 0; c0 < D; c0 += C::kChunk) {
@@ -849,9 +944,6 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
                 #pragma unroll
                 for (int e = 0; e < C::kChunk; ++e)
                     dst[e] = f > 0.f ? __uint_as_float(ov[e]) * f : 0.f;
-            } else {
-                #pragma unroll
-                for (int e = 0; e < C::kChunk; ++e) dst[e] = 0.f;
             }
             if (c0 + C::kChunk >= D && used) {
                 tc_fence_before();
@@ -862,7 +954,8 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
             for (int i = threadIdx.x; i < nrows * C::kChunk; i += 256) {
                 const int rr = i / C::kChunk, c = i % C::kChunk;
                 float sum = 0.f;
-                for (int k = rr >> 5; k < 8; k += quarters) sum += buf[(k * 32 + (rr & 31)) * kLd + c];
+                #pragma unroll 2
+                for (int k = rr >> 5; k < warps; k += quarters) sum += buf[(k * 32 + (rr & 31)) * kLd + c];
                 part_o[((size_t)w.slot + rr) * D + c0 + c] = sum;
             }
             named_bar_sync(1, 256);
@@ -892,7 +985,7 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&sh.kv_full[s], 1);
-            mbar_init(&sh.kv_empty[s], 1);
+            mbar_init(&sh.kv_empty[s], s & 1 ? 1 : 2);   // V: a commit; K: two softmax warps
             mbar_init(&sh.tail[s], 1);
         }
         mbar_init(&sh.drain, 1);
@@ -917,7 +1010,7 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             producer<D, PAGED>(&tmK, &tmV, p, tab, sh, sKV);
         else if (warp == kWarpClear)
             clear_tails<D, PAGED>(p, tab, sh, sKV);
-        else if (warp == kWarpMma && lane_id() == 0)
+        else if (warp == kWarpMma)
             mma_issuer<D, PAGED>(p, tab, sh, smem, sKV);
     }
     __syncwarp();
@@ -1078,6 +1171,7 @@ int launch_any(const SharedArgs &a, cudaStream_t stream) {
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = G;
+    p.G_magic = G > 1 ? (uint32_t)(((1ull << 32) + G - 1) / G) : 0u;
     p.Nq = a.Nq;
     p.Nk = a.Nk;
     p.pairs = (a.Nq * G + kRows - 1) / kRows;
