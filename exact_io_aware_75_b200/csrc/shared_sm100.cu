@@ -24,19 +24,23 @@
 //     (prefix sums over the items) is computed by every CTA for itself in
 //     shared memory, about two microseconds; lengths never come to the host.
 //   * Warp 8 feeds a ring of K and V tiles (128 keys) by TMA, page by page
-//     through the block table, and runs ahead over the items.  Warp 9 issues
-//     the products S = Q K^T and O += P V (tcgen05, O in tensor memory).  Warp
-//     10 clears the V rows behind a sequence's end (they may hold anything,
-//     and P = 0 times NaN is NaN).
-//   * Two softmax warpgroups.  More than 128 rows: each has a tile of 128
-//     rows and sees every key block (as the prefill).  Fewer: both have the
-//     same rows and take the key blocks in turn.  At 64 rows or fewer the
-//     rows stand two or four times in the tile's 128 lanes: a warp can read
-//     only its own 32 lanes of tensor memory, so copy i of the rows takes the
-//     i-th part of each block's keys (P = 0 in the others'), and the
-//     exponentials of 4 rows x 128 keys are spread over four warps instead of
-//     one.  The tensor core would compute the other lanes anyway.  The
-//     copies' and the warpgroups' results are joined through shared memory.
+//     through the block table, and runs ahead over the items.  Warp 10 clears
+//     the V rows behind a sequence's end (they may hold anything, and P = 0
+//     times NaN is NaN).
+//   * Up to 32 rows (a sequence's own pages, a token against its encoder
+//     states): S^T = K Q^T and O^T += V^T P^T, so that the keys (then the head
+//     dim) fill the 128 lanes of the products and N is 16 or 32.  Warp 9
+//     issues S^T up to four blocks ahead, warp 11 O^T.  A softmax thread has
+//     one key and all rows; P^T goes through shared memory.  The two softmax
+//     warpgroups take the shares in turn, so that one starts the next while
+//     the other still finishes its own.
+//   * More rows: S = Q K^T and O += P V as in the prefill, P in tensor memory,
+//     warp 9 issuing both.  More than 128 rows: each warpgroup has a tile of
+//     128 rows and sees every block.  Up to 128: both have the same rows and
+//     take the blocks in turn; their results are joined through shared memory.
+//     Up to 64: the rows stand twice in the tile's 128 lanes, each copy takes
+//     half of a block's keys (P = 0 in the other's), and four warps share the
+//     exponentials instead of two.
 //   * shared_combine_kernel joins the partials of each row.
 #include <climits>
 #include <cuda.h>
@@ -55,7 +59,7 @@ constexpr int kBlockN = 128;        // keys per K/V tile
 constexpr int kPagesPerBlock = kBlockN / kPage;
 constexpr int kRows = 2 * kBlockM;  // rows per item
 constexpr int kThreads = 384;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpClear = 10;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpClear = 10, kWarpMmaPV = 11;
 // Registers: launched with 384 x 168; softmax warpgroups 216, the rest 72
 // (2 * 128 * 216 + 128 * 72 = 64,512).
 constexpr int kRegsSoftmax = 216, kRegsControl = 72;
@@ -66,7 +70,8 @@ constexpr int kMaxSeqs = kSharedMaxSeqs;    // sequences per launch
 constexpr int kMaxGroupItems = 1024;        // group <= 128 heads: at most S/2 + S/2 items
 constexpr int kMaxItems = kSharedMaxItems;
 static_assert(kMaxSeqs + kMaxGroupItems <= kMaxItems, "items of a paged batch");
-constexpr int kFewRows = 16;                // rows the two warpgroups exchange at once
+constexpr int kFewRows = 32;                // rows at most in the transposed form
+constexpr int kSBufs = 4;                   // S^T buffers per warpgroup, 32 columns each
 // Cost of a key block, in half tiles of K/V read from HBM, and of an item
 // besides (its first loads and its epilogue).
 constexpr int kCostBlock = 2, kCostBlock2 = 3, kCostItem = 1;
@@ -77,10 +82,13 @@ struct Cfg {
     static constexpr int kBoxBytes = kBlockM * 128;            // 128 rows x 128 bytes
     static constexpr int kTileBytes = kBlockM * D * 2;
     static constexpr int kStages = D == 128 ? 4 : 8;           // K in the even slots, V in the odd
-    static constexpr int kOffKV = 2 * kTileBytes;
+    // Q of a warpgroup's tile: 32 KB for either head dim.  With few rows: Q's
+    // rows at the start of each box, two buffers of P^T behind them.
+    static constexpr int kQBytes = 32768;
+    static constexpr int kOffKV = 2 * kQBytes;
     static constexpr int kOffTable = kOffKV + kStages * kTileBytes;
     static constexpr uint32_t kColO = 256;                     // O_t at 256 + t*D
-    static constexpr int kChunk = D == 128 ? 32 : 16;          // columns joined at a time
+    static constexpr int kChunk = 32;                          // columns joined at a time
 };
 
 // The plan, in shared memory.
@@ -112,13 +120,20 @@ struct Params {
 struct Shared {
     uint64_t q_full[2];
     uint64_t kv_full[8], kv_empty[8], tail[8];
-    uint64_t s_full[2], p_lo[2], p_hi[2], o_full[2], o_empty[2];
-    uint64_t drain;
+    uint64_t s_full[2], p_lo[2], p_hi[2], o_full[2];
+    uint64_t st_full[2][kSBufs], st_empty[2][kSBufs], pt_full[2][2], pt_empty[2][2];
+    uint64_t drain[2];
     float2 ml[8][32];
     int scan[kThreads / 32];
     uint32_t tmem_base;
     int abort;
 };
+
+// Rows of a P^T buffer (and N of the transposed products): 16 or 32.
+__device__ __forceinline__ int few_n(int rows) { return rows <= 16 ? 16 : 32; }
+
+// P^T buffer b of a warpgroup, within its Q tile.
+__device__ __forceinline__ int few_p(int b) { return b ? 20480 : 4096; }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -332,14 +347,20 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
 struct Work {
     Item it;
     int kb0, kb1;    // key blocks
+    bool few;        // transposed form, by warpgroup `wg`
+    int wg;
     int rep;         // copies of the rows in a tile's lanes
     bool pair;       // two row tiles on every block (else: one, blocks in turn)
     int slot;        // first partial row
+    uint32_t ring;   // ring position of its first K tile
 };
 
 struct Walker {
-    int i, lo, hi, share;
+    int i, lo, hi, share, turn;
+    uint32_t ring;
     __device__ __forceinline__ void begin(const Params &p, const Table &tab) {
+        turn = 0;
+        ring = 0;
         share = blockIdx.x / p.Hkv;
         lo = share * tab.span;
         hi = lo + tab.span;
@@ -361,7 +382,12 @@ struct Walker {
             w.kb1 = min(nb, div_cost(hi - start, cost));
             if (w.kb0 >= w.kb1) continue;
             w.pair = w.it.rows > kBlockM;
-            w.rep = w.it.rows > 64 ? 1 : w.it.rows > 32 ? 2 : 4;
+            w.few = w.it.rows <= kFewRows;
+            w.wg = turn;
+            if (w.few) turn ^= 1;
+            w.rep = w.it.rows > 64 ? 1 : 2;
+            w.ring = ring;
+            ring += 2 * (w.kb1 - w.kb0);
             w.slot = tab.slot[i] + (start >= lo ? 0 : share - start / tab.span) * w.it.rows;
             ++i;
             return true;
@@ -452,15 +478,14 @@ template <int D, bool PAGED>
 __device__ void clear_tails(const Params &p, const Table &tab, Shared &sh, uint8_t *sKV) {
     using C = Cfg<D>;
     const int lane = lane_id();
-    uint32_t it = 0, phase = 0;
+    uint32_t phase = 0;
     Walker walk;
     walk.begin(p, tab);
     Work w;
     while (walk.next<PAGED>(p, tab, w)) {
         const int valid = w.it.keys - (w.kb1 - 1) * kBlockN;
-        it += 2 * (w.kb1 - w.kb0);
         if (!needs_clear<PAGED>(p, w, valid)) continue;
-        const int slot = (it - 1) % C::kStages;       // the share's last V tile
+        const int slot = (w.ring + 2 * (w.kb1 - w.kb0) - 1) % C::kStages;   // the share's last V tile
         if (!mbar_wait_warp(&sh.tail[slot], phase >> slot & 1, &sh.abort)) return;
         phase ^= 1u << slot;
         uint8_t *dst = sKV + slot * C::kTileBytes + valid * 128;
@@ -474,12 +499,14 @@ __device__ void clear_tails(const Params &p, const Table &tab, Shared &sh, uint8
     }
 }
 
-// ------------------------------------------------------------ MMA issuer
-// A whole warp, of which one lane issues.  Commits cost it some 250 cycles
-// each, so a block has two: S's, upon which the softmax warps hand the K slot
+// ------------------------------------------------------------ MMA issuers
+// Whole warps, of which one lane issues.  Commits cost it some 250 cycles
+// each, so there are few: S's, upon which the softmax warps hand the K slot
 // back, and that of the V slot.  Products complete in the order of their
 // issue, so with S of a tile's next block P V of the block before is done;
-// O's own commit comes after a share's last block.
+// O's own commit comes after a share's last block.  O and the Q tile need no
+// barrier of their own: a warpgroup's next Q (and P) arrives only after it
+// has read its O.
 template <int D, bool PAGED>
 __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_t *sQ, uint8_t *sKV) {
     using C = Cfg<D>;
@@ -489,16 +516,15 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
     const uint32_t idPV = idesc_bf16_f32(kBlockM, D, true);
     const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(sKV), 16);
     const uint32_t v_lo = desc_lo(smem_u32(sKV), C::kBoxBytes);
-    constexpr uint32_t kTileStep = C::kTileBytes >> 4;
-    uint32_t q_uses[2] = {0, 0}, p_cnt[2] = {0, 0}, oe_uses[2] = {0, 0};
-    uint32_t it = 0;
+    constexpr uint32_t kTileStep = C::kTileBytes >> 4, kQStep = C::kQBytes >> 4;
+    uint32_t q_uses[2] = {0, 0}, p_cnt[2] = {0, 0}, st_cnt[2] = {0, 0};
     // S_t = Q_t K^T (K-major operands, 128-byte swizzle, 64 columns per box)
     auto issue_s = [&](int t, int slot) {
         if (elect_one()) {
             #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
-                mma_ss_lo(tmem + t * kBlockN, q_lo + t * kTileStep + off, k_lo + slot * kTileStep + off,
+                mma_ss_lo(tmem + t * kBlockN, q_lo + t * kQStep + off, k_lo + slot * kTileStep + off,
                           idS, ks > 0 ? 1u : 0u);
             }
             tc_commit(&sh.s_full[t]);
@@ -507,14 +533,9 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
     };
     // O_t += P_t V, keys 0-63 when they are there, then 64-127
     auto issue_pv = [&](int t, int slot, bool &first, bool last, bool free) -> bool {
-        if (!mbar_wait_warp(&sh.p_lo[t], p_cnt[t] & 1, abort)) return false;
-        if (first) {
-            if (!mbar_wait_warp(&sh.o_empty[t], (oe_uses[t] & 1) ^ 1, abort)) return false;
-            ++oe_uses[t];
-        }
         #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            if (half && !mbar_wait_warp(&sh.p_hi[t], p_cnt[t] & 1, abort)) return false;
+            if (!mbar_wait_warp(half ? &sh.p_hi[t] : &sh.p_lo[t], p_cnt[t] & 1, abort)) return false;
             tc_fence_after();
             if (elect_one()) {
                 #pragma unroll
@@ -538,6 +559,33 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
     Work w;
     while (walk.next<PAGED>(p, tab, w)) {
         const int nb = w.kb1 - w.kb0;
+        uint32_t it = w.ring;
+        if (w.few) {
+            // S^T = K Q^T into the warpgroup's next free buffer
+            const uint32_t id = idesc_bf16_f32(kBlockN, few_n(w.it.rows), false);
+            const uint32_t q = q_lo + w.wg * kQStep;
+            if (!mbar_wait_warp(&sh.q_full[w.wg], q_uses[w.wg] & 1, abort)) goto out;
+            ++q_uses[w.wg];
+            for (int j = 0; j < nb; ++j, it += 2) {
+                const int ks = it % C::kStages;
+                const uint32_t n = st_cnt[w.wg]++;
+                const int buf = n % kSBufs;
+                if (!mbar_wait_warp(&sh.kv_full[ks], (it / C::kStages) & 1, abort)) goto out;
+                if (!mbar_wait_warp(&sh.st_empty[w.wg][buf], ((n / kSBufs) & 1) ^ 1, abort)) goto out;
+                tc_fence_after();
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4;
+                        mma_ss_lo(tmem + w.wg * kBlockN + buf * 32, k_lo + ks * kTileStep + off, q + off,
+                                  id, k > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&sh.st_full[w.wg][buf]);
+                }
+                __syncwarp();
+            }
+            continue;
+        }
         bool first[2] = {true, true};
         for (int t = 0; t < 2; ++t) {
             if (t == 1 && !w.pair && nb == 1) continue;
@@ -582,9 +630,55 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
     }
 out:
     // Wait for every MMA this thread issued before TMEM is released.
-    if (elect_one()) tc_commit(&sh.drain);
+    if (elect_one()) tc_commit(&sh.drain[0]);
     __syncwarp();
-    mbar_drain_wait(&sh.drain, 0);
+    mbar_drain_wait(&sh.drain[0], 0);
+}
+
+// O^T += V^T P^T of the transposed form: V^T is an MN-major A operand (d
+// contiguous), P^T's rows are K-major.  At d = 64 the products' lanes 64-127
+// multiply whatever lies behind the V tile and are not read.
+template <int D, bool PAGED>
+__device__ void mma_issuer_pv(const Params &p, const Table &tab, Shared &sh, uint8_t *sQ, uint8_t *sKV) {
+    using C = Cfg<D>;
+    volatile int *abort = &sh.abort;
+    const uint32_t tmem = sh.tmem_base;
+    const uint32_t v_lo = desc_lo(smem_u32(sKV), C::kBoxBytes);
+    constexpr uint32_t kTileStep = C::kTileBytes >> 4;
+    uint32_t cnt[2] = {0, 0};
+    Walker walk;
+    walk.begin(p, tab);
+    Work w;
+    while (walk.next<PAGED>(p, tab, w)) {
+        if (!w.few) continue;
+        const int nb = w.kb1 - w.kb0, n = few_n(w.it.rows);
+        const uint32_t id = idesc_bf16_f32_ab(kBlockM, n, true, false);
+        uint32_t it = w.ring + 1;
+        for (int j = 0; j < nb; ++j, it += 2) {
+            const int vs = it % C::kStages;
+            const uint32_t c = cnt[w.wg]++;
+            const int b = c & 1;
+            if (!mbar_wait_warp(&sh.kv_full[vs], (it / C::kStages) & 1, abort)) goto out;
+            if (!mbar_wait_warp(&sh.pt_full[w.wg][b], (c >> 1) & 1, abort)) goto out;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t pt = desc_lo(smem_u32(sQ + w.wg * C::kQBytes + few_p(b)), 16);
+                const uint32_t v = v_lo + vs * kTileStep;
+                #pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ss_lo(tmem + C::kColO + w.wg * D, v + ((ks * 2048) >> 4),
+                              pt + (((ks >> 2) * n * 128 + (ks & 3) * 32) >> 4), id,
+                              (ks > 0 || j > 0) ? 1u : 0u);
+                tc_commit(&sh.kv_empty[vs]);
+                tc_commit(&sh.pt_empty[w.wg][b]);
+            }
+            __syncwarp();
+        }
+    }
+out:
+    if (elect_one()) tc_commit(&sh.drain[1]);
+    __syncwarp();
+    mbar_drain_wait(&sh.drain[1], 0);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -681,16 +775,7 @@ template <int D>
 __device__ __forceinline__ void soft_block(Row &r, int rep, int limit, bool first, float sl2,
                                            uint32_t tS, uint32_t tO, Shared &sh, int t) {
     const int q4 = warp_id() & 3;
-    if (rep == 4) {
-        uint32_t pk[16], z[32];
-        soft_part<D, 32>(r, q4 * 32, limit, first, sl2, tS, tO, pk);
-        #pragma unroll
-        for (int i = 0; i < 32; ++i) z[i] = 0u;
-        const uint32_t half = tS + (q4 >> 1) * 64;
-        tmem_st32(tS + (1 - (q4 >> 1)) * 64, z);
-        tmem_st16(half + (q4 & 1) * 16, pk);
-        tmem_st16(half + (1 - (q4 & 1)) * 16, z);
-    } else if (rep == 2) {
+    if (rep == 2) {
         uint32_t pk[32], z[32];
         soft_part<D, 64>(r, (q4 >> 1) * 64, limit, first, sl2, tS, tO, pk);
         #pragma unroll
@@ -750,6 +835,190 @@ __device__ __forceinline__ void soft_block(Row &r, int rep, int limit, bool firs
     }
 }
 
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
+    if constexpr (N == 4) tmem_ld4(addr, r);
+    else if constexpr (N == 8) tmem_ld8(addr, r);
+    else if constexpr (N == 16) tmem_ld16(addr, r);
+    else tmem_ld32(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_n(uint32_t addr, const uint32_t (&r)[N]) {
+    if constexpr (N == 4) tmem_st4(addr, r);
+    else if constexpr (N == 8) tmem_st8(addr, r);
+    else if constexpr (N == 16) tmem_st16(addr, r);
+    else tmem_st32(addr, r);
+}
+
+// Floats as integers of the same order (for an integer maximum over a warp).
+__device__ __forceinline__ int ordered(float x) {
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) {
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// What a warpgroup carries from share to share.
+struct Count {
+    uint32_t s, blocks, o;   // S and P barriers; transposed blocks; O barrier
+};
+
+// A share of up to RN rows, by one warpgroup: thread = key (of S^T), then
+// head-dim index (of O^T).  The reference maxima are the same in all threads.
+// False: a wait ran out (in all threads of the warpgroup alike).
+template <int D, int RN>
+__device__ bool few_rows(const Params &p, const Work &w, Shared &sh, uint8_t *tile, int wg, int kvh,
+                         Count &cnt, float *part_o, float *part_lse) {
+    using C = Cfg<D>;
+    constexpr int N = RN <= 16 ? 16 : 32;
+    const int warp = warp_id(), q4 = warp & 3, lane = lane_id(), tid = threadIdx.x & 127;
+    const int bar = 2 + wg;
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tS = sh.tmem_base + lanes + wg * kBlockN;
+    const uint32_t tO = sh.tmem_base + lanes + C::kColO + wg * D;
+    const int rows = w.it.rows;
+    float *red = reinterpret_cast<float *>(&sh.ml[0][0]) + wg * 256;   // [4 warps][32] of this warpgroup
+    {
+        constexpr int kWords = RN * D / 8, kPer = (kWords + 127) / 128;
+        uint4 qv[kPer];
+        #pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int x = tid + i * 128, row = x / (D / 8), c = x % (D / 8);
+            qv[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows) {
+                const int at = w.it.row0 + row, tok = div_group(p, at);
+                qv[i] = __ldg(reinterpret_cast<const uint4 *>(
+                    p.q + ((size_t)(w.it.tok0 + tok) * p.Hq + kvh * p.G + at - tok * p.G) * D) + c);
+            }
+        }
+        #pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int x = tid + i * 128, row = x / (D / 8), c = x % (D / 8);
+            if (x < kWords)
+                *reinterpret_cast<uint4 *>(tile + (c >> 3) * C::kBoxBytes + row * 128 +
+                                           (((c & 7) ^ (row & 7)) << 4)) = qv[i];
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[wg]);
+    }
+    float m[RN], l[RN];
+    #pragma unroll
+    for (int r = 0; r < RN; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+    }
+    const int key = tid;
+    uint8_t *pt_key = tile + (key >> 6) * (N * 128) + (key & 7) * 2;
+    const int chunk = (key & 63) >> 3;
+    bool ok = true;
+    for (int j = w.kb0; j < w.kb1; ++j) {
+        const uint32_t n = cnt.blocks;
+        const int sb = n % kSBufs, pb = n & 1;
+        float s[RN];
+        bool up = false;
+        ok = ok && mbar_wait_warp(&sh.st_full[wg][sb], (n / kSBufs) & 1, &sh.abort);
+        if (ok) {
+            uint32_t raw[RN];
+            tc_fence_after();
+            tmem_ld_n<RN>(tS + sb * 32, raw);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.st_empty[wg][sb]);
+                if (q4 < 2) mbar_arrive(&sh.kv_empty[(w.ring + 2 * (j - w.kb0)) % C::kStages]);
+            }
+            const bool seen = w.it.keys - j * kBlockN > key;
+            #pragma unroll
+            for (int r = 0; r < RN; ++r) {
+                s[r] = seen ? __uint_as_float(raw[r]) * p.scale_log2 : -INFINITY;
+                up |= s[r] > m[r] + kRescaleThreshold;
+            }
+        }
+        // some key raises a row's maximum by more than the threshold (always in
+        // the first block), or a warp has given up
+        if (named_bar_or(bar, 128, up || !ok)) {
+            if (ok) {
+                #pragma unroll
+                for (int r = 0; r < RN; ++r) {
+                    const int x = __reduce_max_sync(0xffffffffu, ordered(s[r]));
+                    if (lane == 0) red[q4 * 32 + r] = unordered(x);
+                }
+                // P V of the blocks before, which O holds
+                if (j > w.kb0) ok = mbar_wait_warp(&sh.pt_empty[wg][pb ^ 1], ((n - 1) >> 1) & 1, &sh.abort);
+            }
+            if (!named_bar_and(bar, 128, ok)) return false;
+            tc_fence_after();
+            float alpha[RN];
+            #pragma unroll
+            for (int r = 0; r < RN; ++r) {
+                const float top = fmaxf(fmaxf(red[r], red[32 + r]), fmaxf(red[64 + r], red[96 + r]));
+                const float m_new = fmaxf(m[r], top);
+                alpha[r] = m_new == -INFINITY ? 1.f : ex2(m[r] - m_new);
+                l[r] *= alpha[r];
+                m[r] = m_new;
+            }
+            if (j > w.kb0) {
+                uint32_t ov[RN];
+                tmem_ld_n<RN>(tO, ov);
+                tmem_wait_ld();
+                #pragma unroll
+                for (int r = 0; r < RN; ++r) ov[r] = __float_as_uint(__uint_as_float(ov[r]) * alpha[r]);
+                tmem_st_n<RN>(tO, ov);
+                tmem_wait_st();
+            }
+        }
+        // P^T's buffer of two blocks ago
+        ok = mbar_wait_warp(&sh.pt_empty[wg][pb], ((n >> 1) & 1) ^ 1, &sh.abort);
+        if (ok) {
+            uint8_t *dst = pt_key + few_p(pb);
+            #pragma unroll
+            for (int r = 0; r < RN; r += 2) {
+                const float p0 = ex2(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+                const float p1 = ex2(s[r + 1] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]));
+                l[r] += p0;
+                l[r + 1] += p1;
+                const uint32_t pk = pack_bf16(p0, p1);     // off by at most 2^-8 relative
+                *reinterpret_cast<uint16_t *>(dst + r * 128 + ((chunk ^ (r & 7)) << 4)) = (uint16_t)pk;
+                *reinterpret_cast<uint16_t *>(dst + (r + 1) * 128 + ((chunk ^ ((r + 1) & 7)) << 4)) =
+                    (uint16_t)(pk >> 16);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.pt_full[wg][pb]);
+        }
+        ++cnt.blocks;
+    }
+    // the last P V: its buffer comes free
+    ok = ok && mbar_wait_warp(&sh.pt_empty[wg][(cnt.blocks - 1) & 1], ((cnt.blocks - 1) >> 1) & 1, &sh.abort);
+    #pragma unroll
+    for (int r = 0; r < RN; ++r) {
+        #pragma unroll
+        for (int off = 16; off; off >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
+        if (lane == 0) red[128 + q4 * 32 + r] = l[r];
+    }
+    if (!named_bar_and(bar, 128, ok)) return false;
+    tc_fence_after();
+    uint32_t ov[RN];
+    tmem_ld_n<RN>(tO, ov);
+    tmem_wait_ld();
+    #pragma unroll
+    for (int r = 0; r < RN; ++r) {
+        const float sum = (red[128 + r] + red[160 + r]) + (red[192 + r] + red[224 + r]);
+        if (r < rows) {
+            if (tid < D)
+                part_o[((size_t)w.slot + r) * D + tid] =
+                    sum > 0.f ? __uint_as_float(ov[r]) / sum : 0.f;
+            if (tid == r) part_lse[(size_t)w.slot + r] = sum > 0.f ? m[r] + __log2f(sum) : -INFINITY;
+        }
+    }
+    return true;
+}
+
 template <int D, bool PAGED>
 __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_t *sQ) {
     using C = Cfg<D>;
@@ -762,30 +1031,26 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
     const uint32_t tO = sh.tmem_base + lanes + C::kColO + t * D;
     float *part_o = p.part_o + (size_t)kvh * p.cap * D;
     float *part_lse = p.part_lse + (size_t)kvh * p.cap;
-    uint32_t s_cnt = 0, o_cnt = 0, it = 0;
-    // This thread's row of a share's Q tile, in registers: asked for while the
-    // share before is joined.
-    uint4 qv[D / 8];
-    auto load_q = [&](const Work &w) {
-        const int tile0 = w.pair ? t * kBlockM : 0;
-        const int lr = r & (kBlockM / w.rep - 1), row = w.it.row0 + tile0 + lr;
-        if (lr < min(kBlockM, w.it.rows - tile0)) {
-            const int tok = div_group(p, row);
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.q + ((size_t)(w.it.tok0 + tok) * p.Hq + kvh * p.G + row - tok * p.G) * D);
-            #pragma unroll
-            for (int c = 0; c < D / 8; ++c) qv[c] = __ldg(src + c);
-        } else {
-            #pragma unroll
-            for (int c = 0; c < D / 8; ++c) qv[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
+    Count cnt{0, 0, 0};
     Walker walk;
     walk.begin(p, tab);
-    Work w, after;
-    bool have = walk.next<PAGED>(p, tab, w);
-    if (have) load_q(w);
-    for (; have; w = after) {
+    Work w;
+    bool alive = true;
+    while (walk.next<PAGED>(p, tab, w)) {
+        if (w.few) {
+            if (w.wg != t || !alive) continue;
+            uint8_t *tile = sQ + t * C::kQBytes;
+            alive = w.it.rows <= 4    ? few_rows<D, 4>(p, w, sh, tile, t, kvh, cnt, part_o, part_lse)
+                    : w.it.rows <= 8  ? few_rows<D, 8>(p, w, sh, tile, t, kvh, cnt, part_o, part_lse)
+                    : w.it.rows <= 16 ? few_rows<D, 16>(p, w, sh, tile, t, kvh, cnt, part_o, part_lse)
+                                      : few_rows<D, 32>(p, w, sh, tile, t, kvh, cnt, part_o, part_lse);
+            continue;
+        }
+        if (!alive) {
+            // (this warpgroup gave up: the other one must not wait for it below)
+            named_bar_and(1, 256, false);
+            break;
+        }
         const int step = w.pair ? 1 : 2;
         const int j0 = w.kb0 + (w.pair ? 0 : t);
         const bool used = j0 < w.kb1;
@@ -795,25 +1060,33 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
         const int lr = r & (copy - 1);                    // this thread's row of the tile
         const bool work = (q4 * 32 & (copy - 1)) < nrows; // some lane of the warp has a row
         bool ok = true;
-        if (used) {                                       // swizzled as TMA would write them
-            uint8_t *dst = sQ + t * C::kTileBytes + r * 128;
+        if (used) {                                       // Q, swizzled as TMA would write it
+            uint4 qv[D / 8];
+            const int at = w.it.row0 + tile0 + lr, tok = div_group(p, at);
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + ((size_t)(w.it.tok0 + tok) * p.Hq + kvh * p.G + at - tok * p.G) * D);
+            #pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                qv[c] = lr < nrows ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            uint8_t *dst = sQ + t * C::kQBytes + r * 128;
             #pragma unroll
             for (int c = 0; c < D / 8; ++c)
                 *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBoxBytes + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
             fence_proxy_async_smem();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full[t]);
         }
         Row row{-INFINITY, 0.f};
         for (int j = j0; j < w.kb1 && ok; j += step) {
-            ok = mbar_wait_warp(&sh.s_full[t], s_cnt & 1, &sh.abort);
+            ok = mbar_wait_warp(&sh.s_full[t], cnt.s & 1, &sh.abort);
             if (!ok) break;
-            ++s_cnt;
+            ++cnt.s;
             tc_fence_after();
             // the block's K slot, handed back by two warps: one of each tile
             // where both read it, else two of this one
             if (lane == 0 && q4 < (w.pair ? 1 : 2))
-                mbar_arrive(&sh.kv_empty[(it + 2 * (j - w.kb0)) % C::kStages]);
+                mbar_arrive(&sh.kv_empty[(w.ring + 2 * (j - w.kb0)) % C::kStages]);
             if (work) {
                 soft_block<D>(row, w.rep, w.it.keys - j * kBlockN, j == j0, p.scale_log2, tS, tO, sh, t);
             } else {
@@ -826,13 +1099,10 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
                 }
             }
         }
-        have = walk.next<PAGED>(p, tab, after);
-        if (have) load_q(after);
         if (ok && used) {
-            ok = mbar_wait_warp(&sh.o_full[t], o_cnt++ & 1, &sh.abort);
+            ok = mbar_wait_warp(&sh.o_full[t], cnt.o++ & 1, &sh.abort);
             tc_fence_after();
         }
-        it += 2 * (w.kb1 - w.kb0);
         if (w.pair) {
             // each row has one thread
             if (ok && work) {
@@ -855,9 +1125,6 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
                 }
                 if (lr < nrows) part_lse[at] = row.l > 0.f ? row.m + __log2f(row.l) : -INFINITY;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.o_empty[t]);
             // the warps leave the loop together, or a later barrier would not fill
             if (!named_bar_and(1, 256, ok)) break;
             continue;
@@ -885,55 +1152,8 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
             part_lse[(size_t)w.slot + r] = L > 0.f ? M + __log2f(L) : -INFINITY;
         float *buf = reinterpret_cast<float *>(sQ);
         const int warps = w.kb1 - w.kb0 > 1 ? 8 : 4;      // (of one block, the first warpgroup only)
-        if (nrows <= kFewRows) {
-            // Few rows (every warp has all of them in its first lanes): whole
-            // rows at once, 16-byte words turned by the row against conflicts.
-            constexpr int kWords = D / 4;
-            static_assert(8 * kFewRows * D * 4 <= 2 * C::kTileBytes, "exchange within Q's tiles");
-            float4 *b4 = reinterpret_cast<float4 *>(buf);
-            if (used) {
-                #pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    uint32_t ov[64];
-                    tmem_ld32(tO + c0, ov);
-                    tmem_ld32(tO + c0 + 32, ov + 32);
-                    tmem_wait_ld();
-                    if (lane < nrows) {
-                        #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (f > 0.f)
-                                v = make_float4(__uint_as_float(ov[4 * e]) * f, __uint_as_float(ov[4 * e + 1]) * f,
-                                                __uint_as_float(ov[4 * e + 2]) * f, __uint_as_float(ov[4 * e + 3]) * f);
-                            b4[(warp * kFewRows + lane) * kWords + ((c0 / 4 + e + lane) & (kWords - 1))] = v;
-                        }
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.o_empty[t]);
-            }
-            named_bar_sync(1, 256);
-            for (int i = threadIdx.x; i < nrows * kWords; i += 256) {
-                const int rr = i / kWords, c = i % kWords;
-                const float4 *src = b4 + rr * kWords + ((c + rr) & (kWords - 1));
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < warps) {
-                        const float4 v = src[k * kFewRows * kWords];
-                        sum.x += v.x;
-                        sum.y += v.y;
-                        sum.z += v.z;
-                        sum.w += v.w;
-                    }
-                reinterpret_cast<float4 *>(part_o + ((size_t)w.slot + rr) * D)[c] = sum;
-            }
-            named_bar_sync(1, 256);
-            continue;
-        }
         constexpr int kLd = C::kChunk + 1;
-        static_assert(8 * 32 * kLd * 4 <= 2 * C::kTileBytes, "exchange within Q's tiles");
+        static_assert(8 * 32 * kLd * 4 <= 2 * C::kQBytes, "exchange within Q's tiles");
         for (int c0 = 0; c0 < D; c0 += C::kChunk) {
             float *dst = buf + (warp * 32 + lane) * kLd;
             if (used && work) {
@@ -945,16 +1165,10 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
                 for (int e = 0; e < C::kChunk; ++e)
                     dst[e] = f > 0.f ? __uint_as_float(ov[e]) * f : 0.f;
             }
-            if (c0 + C::kChunk >= D && used) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.o_empty[t]);
-            }
             named_bar_sync(1, 256);
             for (int i = threadIdx.x; i < nrows * C::kChunk; i += 256) {
                 const int rr = i / C::kChunk, c = i % C::kChunk;
                 float sum = 0.f;
-                #pragma unroll 2
                 for (int k = rr >> 5; k < warps; k += quarters) sum += buf[(k * 32 + (rr & 31)) * kLd + c];
                 part_o[((size_t)w.slot + rr) * D + c0 + c] = sum;
             }
@@ -981,14 +1195,21 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             mbar_init(&sh.p_lo[t], 4);
             mbar_init(&sh.p_hi[t], 4);
             mbar_init(&sh.o_full[t], 1);
-            mbar_init(&sh.o_empty[t], 4);
+            mbar_init(&sh.drain[t], 1);
+            for (int b = 0; b < kSBufs; ++b) {
+                mbar_init(&sh.st_full[t][b], 1);
+                mbar_init(&sh.st_empty[t][b], 4);
+            }
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&sh.pt_full[t][b], 4);
+                mbar_init(&sh.pt_empty[t][b], 1);
+            }
         }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&sh.kv_full[s], 1);
             mbar_init(&sh.kv_empty[s], s & 1 ? 1 : 2);   // V: a commit; K: two softmax warps
             mbar_init(&sh.tail[s], 1);
         }
-        mbar_init(&sh.drain, 1);
         sh.abort = 0;
         fence_barrier_init();
     }
@@ -1012,6 +1233,8 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             clear_tails<D, PAGED>(p, tab, sh, sKV);
         else if (warp == kWarpMma)
             mma_issuer<D, PAGED>(p, tab, sh, smem, sKV);
+        else
+            mma_issuer_pv<D, PAGED>(p, tab, sh, smem, sKV);
     }
     __syncwarp();
     tc_fence_before();
