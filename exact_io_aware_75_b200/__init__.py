@@ -175,14 +175,21 @@ def version() -> int:
     return int(_lib.fa_version())
 
 
+# The argument checks run on every call, next to kernels of a few microseconds:
+# plain integers for pointers, the raw stream handle, no objects made in passing.
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(rc: int, where: str):
@@ -191,6 +198,9 @@ def _check(rc: int, where: str):
 
 
 def _need(t, dtype, ndim, name):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise FAError(FA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -460,12 +470,13 @@ def bwd_varlen(q, k, v, o, dout, lse, cu_seqlens, max_seqlen, causal=False, wind
     return dq, dk, dv
 
 
-def _out_pair(out, lse, o_shape, lse_shape, out_dtype, return_lse, device):
-    """The output tensors of a forward call: given ones checked, missing ones made."""
+def _out_pair(out, lse, o_shape, lse_shape, out_dtype, return_lse, like):
+    """The output tensors of a forward call: given ones checked, missing ones made on
+    like's device."""
     if out is None:
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise FAError(FA_ERR_INVALID_ARG, f"out_dtype {out_dtype}")
-        out = torch.empty(o_shape, dtype=out_dtype, device=device)
+        out = like.new_empty(o_shape, dtype=out_dtype)
     else:
         _need(out, torch.float32 if out.dtype == torch.float32 else torch.bfloat16, len(o_shape), "out")
         if tuple(out.shape) != tuple(o_shape):
@@ -475,15 +486,15 @@ def _out_pair(out, lse, o_shape, lse_shape, out_dtype, return_lse, device):
         if tuple(lse.shape) != tuple(lse_shape):
             raise FAError(FA_ERR_INVALID_ARG, "lse shape")
     elif return_lse:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
+        lse = like.new_empty(lse_shape, dtype=torch.float32)
     return out, lse, FA_OUT_FP32 if out.dtype == torch.float32 else FA_OUT_BF16
 
 
-def _decode_out(out, lse, o_shape, lse_shape, return_lse, device):
+def _decode_out(out, lse, o_shape, lse_shape, return_lse, like):
     """As _out_pair, for calls whose O is bf16."""
     if out is not None and getattr(out, "dtype", None) != torch.bfloat16:
         raise FAError(FA_ERR_INVALID_ARG, "out must be torch.bfloat16")
-    return _out_pair(out, lse, o_shape, lse_shape, torch.bfloat16, return_lse, device)[:2]
+    return _out_pair(out, lse, o_shape, lse_shape, torch.bfloat16, return_lse, like)[:2]
 
 
 def _same(t, ref, name):
@@ -516,7 +527,7 @@ def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, ou
         _need_ints((B,), "seq_lens_k", seq_lens_k)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out, lse, od = _out_pair(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), out_dtype, return_lse, q.device)
+    out, lse, od = _out_pair(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), out_dtype, return_lse, q)
     with _device_of(q, k=k, v=v, seq_lens_k=seq_lens_k, out=out, lse=lse):
         _check(_lib.fa_fwd_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(seq_lens_k),
                                  B, Hq, Hkv, Nq, Nk, d, float(scale), od, _stream(stream)),
@@ -535,7 +546,7 @@ def fwd_varlen_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
     _need_ints(cu_seqlens_q.shape, "cu_seqlens_k", cu_seqlens_k)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out, lse, od = _out_pair(out, lse, (Tq, Hq, d), (Hq, Tq), out_dtype, return_lse, q.device)
+    out, lse, od = _out_pair(out, lse, (Tq, Hq, d), (Hq, Tq), out_dtype, return_lse, q)
     with _device_of(q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out,
                     lse=lse):
         _check(_lib.fa_fwd_varlen_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
@@ -563,7 +574,7 @@ def bwd_cross(q, k, v, o, dout, lse, seq_lens_k=None, scale=None, dq=None, dk=No
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     dq, dk, dv = _like(dq, q, "dq"), _like(dk, k, "dk"), _like(dv, v, "dv")
-    workspace = _bytes_of(workspace, bwd_workspace_bytes(B * Nq, Hq, d), q.device)
+    workspace = _bytes_of(workspace, bwd_workspace_bytes(B * Nq, Hq, d), q)
     with _device_of(q, k=k, v=v, o=o, dout=dout, lse=lse, seq_lens_k=seq_lens_k, dq=dq, dk=dk,
                     dv=dv, workspace=workspace):
         _check(_lib.fa_bwd_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
@@ -591,7 +602,7 @@ def bwd_varlen_cross(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seql
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     dq, dk, dv = _like(dq, q, "dq"), _like(dk, k, "dk"), _like(dv, v, "dv")
-    workspace = _bytes_of(workspace, bwd_workspace_bytes(Tq, Hq, d), q.device)
+    workspace = _bytes_of(workspace, bwd_workspace_bytes(Tq, Hq, d), q)
     with _device_of(q, k=k, v=v, o=o, dout=dout, lse=lse, cu_seqlens_q=cu_seqlens_q,
                     cu_seqlens_k=cu_seqlens_k, dq=dq, dk=dk, dv=dv, workspace=workspace):
         _check(_lib.fa_bwd_varlen_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
@@ -633,8 +644,8 @@ def decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_
             raise FAError(FA_ERR_INVALID_ARG, "sinks shape")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out, lse = _decode_out(out, lse, (S, Hq, d), (S, Hq), return_lse, q.device)
-    workspace = _bytes_of(workspace, decode_shared_workspace_bytes(S, Hq, max(Hkv, 1), d), q.device)
+    out, lse = _decode_out(out, lse, (S, Hq, d), (S, Hq), return_lse, q)
+    workspace = _bytes_of(workspace, decode_shared_workspace_bytes(S, Hq, max(Hkv, 1), d), q)
     with _device_of(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
                     seq_lens=seq_lens, cu_groups=cu_groups, prefix_lens=prefix_lens, sinks=sinks,
                     out=out, lse=lse, workspace=workspace):
@@ -663,9 +674,8 @@ def decode_cross(q, k, v, seq_lens_k=None, scale=None, out=None, lse=None, retur
         _need_ints((B,), "seq_lens_k", seq_lens_k)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out, lse = _decode_out(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), return_lse, q.device)
-    workspace = _bytes_of(workspace, decode_cross_workspace_bytes(B, Hq, max(Hkv, 1), Nq, d),
-                          q.device)
+    out, lse = _decode_out(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), return_lse, q)
+    workspace = _bytes_of(workspace, decode_cross_workspace_bytes(B, Hq, max(Hkv, 1), Nq, d), q)
     with _device_of(q, k=k, v=v, seq_lens_k=seq_lens_k, out=out, lse=lse, workspace=workspace):
         _check(_lib.fa_decode_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens_k), _ptr(out),
                                     _ptr(lse), B, Hq, Hkv, Nq, Nk, d, float(scale),
@@ -781,14 +791,16 @@ def decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, scale=None,
     return out, lse
 
 
+_same_device = contextlib.nullcontext()
+
+
 def _device_of(first, **others):
     """A context in which the device of `first` is current; the others must be on it."""
+    device = first.get_device()
     for name, t in others.items():
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != device:
             raise FAError(FA_ERR_INVALID_ARG, f"{name} is on {t.device}, not {first.device}")
-    if first.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(first.device)
+    return _same_device if device == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _need_cache(k_cache, v_cache, k_scale, v_scale):
@@ -816,13 +828,13 @@ def _need_cache(k_cache, v_cache, k_scale, v_scale):
 
 def _need_ints(shape, name, t):
     _need(t, torch.int32, len(shape), name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise FAError(FA_ERR_INVALID_ARG, f"{name} shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
-def _bytes_of(workspace, need, device):
+def _bytes_of(workspace, need, like):
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        return like.new_empty(max(need, 1), dtype=torch.uint8)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise FAError(FA_ERR_WORKSPACE, "workspace must be a contiguous CUDA tensor")
     return workspace
@@ -919,7 +931,7 @@ def cache_collect(block_table, seq_lens, free_pages, free_count, page_size=16, w
     P = free_pages.shape[0]
     _need_ints((S,), "seq_lens", seq_lens)
     _need_ints((1,), "free_count", free_count)
-    workspace = _bytes_of(workspace, cache_collect_workspace_bytes(P), block_table.device)
+    workspace = _bytes_of(workspace, cache_collect_workspace_bytes(P), block_table)
     with _device_of(block_table, seq_lens=seq_lens, free_pages=free_pages, free_count=free_count,
                     workspace=workspace):
         _check(_lib.fa_cache_collect(_ptr(block_table), _ptr(seq_lens), S, maxp, P,
@@ -945,7 +957,7 @@ def cache_compact(k_cache, v_cache, block_table, seq_lens, block_table_out, free
     _need_ints((S, maxp), "block_table_out", block_table_out)
     _need_ints((P,), "free_pages", free_pages)
     _need_ints((1,), "free_count", free_count)
-    workspace = _bytes_of(workspace, cache_compact_workspace_bytes(P), k_cache.device)
+    workspace = _bytes_of(workspace, cache_compact_workspace_bytes(P), k_cache)
     with _device_of(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
                     block_table=block_table, seq_lens=seq_lens, block_table_out=block_table_out,
                     free_pages=free_pages, free_count=free_count, workspace=workspace):
