@@ -42,6 +42,7 @@
 //     half of a block's keys (P = 0 in the other's), and four warps share the
 //     exponentials instead of two.
 //   * shared_combine_kernel joins the partials of each row.
+#include <atomic>
 #include <climits>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -185,6 +186,11 @@ __device__ __forceinline__ Item get_item(const Params &p, const Table &tab, int 
     return w;
 }
 
+template <bool PAGED>
+__device__ __forceinline__ Item item_of(const Params &p, const Table &tab, int i) {
+    return get_item<PAGED>(p, tab, i);
+}
+
 // x / G for the rows of a launch (G_magic = ceil(2^32 / G), exact as x * G < 2^32).
 __device__ __forceinline__ int div_group(const Params &p, int x) {
     return p.G == 1 ? x : (int)__umulhi((uint32_t)x, p.G_magic);
@@ -198,11 +204,16 @@ static_assert(kCostBlock == 2 && kCostBlock2 == 3, "div_cost");
 
 __device__ __forceinline__ int block_cost(int rows) { return rows > kBlockM ? kCostBlock2 : kCostBlock; }
 
+// The plan and the walk over the shares run once or a few times per CTA: what
+// they cost is fetching their instructions.  Their loops are not unrolled and
+// their parts are functions of their own, one copy for all warps (inlined and
+// unrolled, the plan took 3.5 us where it now takes FIXME).
+
 // Exclusive prefix sum over the block's threads; `total` gets the sum.
 __device__ __forceinline__ int block_scan(int x, int *s_warp, int &total) {
     const int lane = lane_id(), warp = warp_id();
     int inc = x;
-    #pragma unroll
+    #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
@@ -210,14 +221,20 @@ __device__ __forceinline__ int block_scan(int x, int *s_warp, int &total) {
     __syncthreads();
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    int before = 0;
-    total = 0;
-    #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += s_warp[w];
-        total += s_warp[w];
+    const int sum = lane < kThreads / 32 ? s_warp[lane] : 0;
+    total = __reduce_add_sync(0xffffffffu, sum);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0) + inc - x;
+}
+
+// The group of sequence s, or -1.
+__device__ __forceinline__ int group_of(const int *cu, int ng, int s) {
+    int lo = 0, hi = ng;
+    #pragma unroll 1
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= s) lo = mid; else hi = mid;
     }
-    return before + inc - x;
+    return ng > 0 && cu[lo] <= s && s < cu[lo + 1] ? lo : -1;
 }
 
 // All threads of the block; ends with a barrier.  `scratch`: room for
@@ -230,6 +247,7 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     int ni = 0, ng = PAGED ? p.num_groups : 0;
     int *cu = scratch, *least = cu + kMaxSeqs + 1, *prefix = least + kMaxSeqs;
     if (PAGED && ng > 0) {
+        #pragma unroll 1
         for (int g = tid; g <= ng; g += kThreads) {
             cu[g] = __ldg(p.cu_groups + g);
             if (g < ng) {
@@ -238,6 +256,7 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
             }
         }
     }
+    #pragma unroll 1
     for (int s = tid; s < p.S; s += kThreads) {
         tab.keys[s] = good_length<PAGED>(p, p.lens ? __ldg(p.lens + s) : p.Nk);
         tab.own[s] = 0;
@@ -245,26 +264,21 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     if (PAGED && ng > 0) {
         __syncthreads();
         bool bad = false;
+        #pragma unroll 1
         for (int g = tid; g < ng; g += kThreads)
             bad |= cu[g] < 0 || cu[g + 1] < cu[g] || cu[g + 1] > p.S;
         if (__syncthreads_or(bad)) {       // unusable groups: every sequence by itself
             if (lead && tid == 0) report_error(kDevErrInput);
             ng = 0;
         }
-        auto group_of = [&](int s) -> int {
-            int lo = 0, hi = ng;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (cu[mid] <= s) lo = mid; else hi = mid;
-            }
-            return ng > 0 && cu[lo] <= s && s < cu[lo + 1] ? lo : -1;
-        };
         // no more is shared than the group's shortest sequence has
+        #pragma unroll 1
         for (int s = tid; s < p.S; s += kThreads) {
-            const int g = group_of(s);
+            const int g = group_of(cu, ng, s);
             if (g >= 0) atomicMin(&least[g], tab.keys[s]);
         }
         __syncthreads();
+        #pragma unroll 1
         for (int g0 = 0; g0 < ng; g0 += kThreads) {
             const int g = g0 + tid;
             int items = 0, pages = 0;
@@ -286,17 +300,20 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
                 prefix[g] = pages > 0 ? base : -1;       // now the group's first item
                 tab.cu[g] = (uint16_t)cu[g];
                 if (g == ng - 1) tab.cu[ng] = (uint16_t)cu[ng];
+                #pragma unroll 1
                 for (int r = 0; r < items; ++r) tab.gi[base + r] = (uint32_t)g | (uint32_t)r << 16;
             }
         }
         __syncthreads();
+        #pragma unroll 1
         for (int s = tid; s < p.S; s += kThreads) {
-            const int g = group_of(s), pages = g >= 0 ? least[g] : 0;
+            const int g = group_of(cu, ng, s), pages = g >= 0 ? least[g] : 0;
             tab.own[s] = pages;
             tab.keys[s] -= pages * kPage;
             if (lead) p.seqs[s] = make_int4(ni + s, g >= 0 ? prefix[g] : -1, g >= 0 ? cu[g] : 0, 0);
         }
     } else if (PAGED && lead) {
+        #pragma unroll 1
         for (int s = tid; s < p.S; s += kThreads) p.seqs[s] = make_int4(s, -1, 0, 0);
     }
     const int N = PAGED ? ni + p.S : p.S * p.pairs;
@@ -308,8 +325,9 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     // cost before each item; a thread has `per` consecutive ones
     const int per = ceil_div(N, kThreads), i0 = min(N, tid * per), i1 = min(N, i0 + per);
     int sum = 0, total;
+    #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-        const Item w = get_item<PAGED>(p, tab, i);
+        const Item w = item_of<PAGED>(p, tab, i);
         tab.start[i] = sum;
         if (w.keys > 0) sum += ceil_div(w.keys, kBlockN) * block_cost(w.rows) + kCostItem;
     }
@@ -317,8 +335,9 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     // (every share must hold the start of a block of any item it lies inside)
     const int span = max(kCostBlock2, ceil_div(total, p.n));
     int rows = 0;
+    #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-        const Item w = get_item<PAGED>(p, tab, i);
+        const Item w = item_of<PAGED>(p, tab, i);
         const int start = tab.start[i] + before;
         tab.start[i] = start;
         int parts = 0;
@@ -331,10 +350,11 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     }
     int all;
     const int slot0 = block_scan(rows, s_warp, all);
+    #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         tab.slot[i] += slot0;
         if (lead) {
-            const Item w = get_item<PAGED>(p, tab, i);
+            const Item w = item_of<PAGED>(p, tab, i);
             const int next = i + 1 < i1 ? tab.slot[i + 1] + slot0 : slot0 + rows;
             p.items[i] = make_int4(tab.slot[i], (next - tab.slot[i]) / w.rows, w.rows, 0);
         }
@@ -365,6 +385,7 @@ struct Walker {
         lo = share * tab.span;
         hi = lo + tab.span;
         int a = 0, b = tab.num_items;          // the last item that starts at or before lo
+        #pragma unroll 1
         while (b - a > 1) {
             const int mid = (a + b) >> 1;
             if (tab.start[mid] <= lo) a = mid; else b = mid;
@@ -373,6 +394,7 @@ struct Walker {
     }
     template <bool PAGED>
     __device__ __forceinline__ bool next(const Params &p, const Table &tab, Work &w) {
+        #pragma unroll 1
         for (; i < tab.num_items; ++i) {
             const int start = tab.start[i];
             if (start >= hi) return false;
@@ -850,13 +872,25 @@ __device__ __forceinline__ void tmem_st_n(uint32_t addr, const uint32_t (&r)[N])
     else tmem_st32(addr, r);
 }
 
-// Floats as integers of the same order (for an integer maximum over a warp).
-__device__ __forceinline__ int ordered(float x) {
-    const int i = __float_as_int(x);
-    return i ^ ((i >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float unordered(int i) {
-    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+// Sums of N values over a warp; lane l gets that of value l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+    #pragma unroll
+    for (int m = 16, n = N; m >= 1; m >>= 1) {
+        if (n > 1) {
+            const bool up = (lane & m) != 0;
+            n >>= 1;
+            #pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < n) {
+                    const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+        }
+    }
+    return v[0];
 }
 
 // What a warpgroup carries from share to share.
@@ -904,10 +938,12 @@ __device__ bool few_rows(const Params &p, const Work &w, Shared &sh, uint8_t *ti
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full[wg]);
     }
+    // (a finite start: no score is below it but -inf, whose P is 0 either way)
+    constexpr float kLowest = -3.0e38f;
     float m[RN], l[RN];
     #pragma unroll
     for (int r = 0; r < RN; ++r) {
-        m[r] = -INFINITY;
+        m[r] = kLowest;
         l[r] = 0.f;
     }
     const int key = tid;
@@ -942,22 +978,25 @@ __device__ bool few_rows(const Params &p, const Work &w, Shared &sh, uint8_t *ti
         // the first block), or a warp has given up
         if (named_bar_or(bar, 128, up || !ok)) {
             if (ok) {
+                float top = 0.f;               // lane r: row r's
                 #pragma unroll
                 for (int r = 0; r < RN; ++r) {
-                    const int x = __reduce_max_sync(0xffffffffu, ordered(s[r]));
-                    if (lane == 0) red[q4 * 32 + r] = unordered(x);
+                    const float x = warp_max(s[r]);
+                    if (lane == r) top = x;
                 }
+                if (lane < RN) red[q4 * 32 + lane] = top;
                 // P V of the blocks before, which O holds
                 if (j > w.kb0) ok = mbar_wait_warp(&sh.pt_empty[wg][pb ^ 1], ((n - 1) >> 1) & 1, &sh.abort);
             }
             if (!named_bar_and(bar, 128, ok)) return false;
             tc_fence_after();
+            const int lr = lane & (RN - 1);
+            const float top = fmaxf(fmaxf(red[lr], red[32 + lr]), fmaxf(red[64 + lr], red[96 + lr]));
             float alpha[RN];
             #pragma unroll
             for (int r = 0; r < RN; ++r) {
-                const float top = fmaxf(fmaxf(red[r], red[32 + r]), fmaxf(red[64 + r], red[96 + r]));
-                const float m_new = fmaxf(m[r], top);
-                alpha[r] = m_new == -INFINITY ? 1.f : ex2(m[r] - m_new);
+                const float m_new = fmaxf(m[r], __shfl_sync(0xffffffffu, top, r));
+                alpha[r] = ex2(m[r] - m_new);
                 l[r] *= alpha[r];
                 m[r] = m_new;
             }
@@ -977,8 +1016,7 @@ __device__ bool few_rows(const Params &p, const Work &w, Shared &sh, uint8_t *ti
             uint8_t *dst = pt_key + few_p(pb);
             #pragma unroll
             for (int r = 0; r < RN; r += 2) {
-                const float p0 = ex2(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-                const float p1 = ex2(s[r + 1] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]));
+                const float p0 = ex2(s[r] - m[r]), p1 = ex2(s[r + 1] - m[r + 1]);
                 l[r] += p0;
                 l[r + 1] += p1;
                 const uint32_t pk = pack_bf16(p0, p1);     // off by at most 2^-8 relative
@@ -995,26 +1033,23 @@ __device__ bool few_rows(const Params &p, const Work &w, Shared &sh, uint8_t *ti
     }
     // the last P V: its buffer comes free
     ok = ok && mbar_wait_warp(&sh.pt_empty[wg][(cnt.blocks - 1) & 1], ((cnt.blocks - 1) >> 1) & 1, &sh.abort);
-    #pragma unroll
-    for (int r = 0; r < RN; ++r) {
-        #pragma unroll
-        for (int off = 16; off; off >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
-        if (lane == 0) red[128 + q4 * 32 + r] = l[r];
-    }
+    const float mine = warp_sums<RN>(l, lane);
+    if ((lane & (32 / RN - 1)) == 0) red[128 + q4 * 32 + lane / (32 / RN)] = mine;
     if (!named_bar_and(bar, 128, ok)) return false;
     tc_fence_after();
     uint32_t ov[RN];
     tmem_ld_n<RN>(tO, ov);
     tmem_wait_ld();
+    const int lr = lane & (RN - 1);            // lane r: row r's sum
+    const float sum = (red[128 + lr] + red[160 + lr]) + (red[192 + lr] + red[224 + lr]);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    float *dst = part_o + (size_t)w.slot * D + tid;
     #pragma unroll
     for (int r = 0; r < RN; ++r) {
-        const float sum = (red[128 + r] + red[160 + r]) + (red[192 + r] + red[224 + r]);
-        if (r < rows) {
-            if (tid < D)
-                part_o[((size_t)w.slot + r) * D + tid] =
-                    sum > 0.f ? __uint_as_float(ov[r]) / sum : 0.f;
-            if (tid == r) part_lse[(size_t)w.slot + r] = sum > 0.f ? m[r] + __log2f(sum) : -INFINITY;
-        }
+        const float f = __shfl_sync(0xffffffffu, inv, r);
+        if (r < rows && tid < D) dst[r * D] = __uint_as_float(ov[r]) * f;
+        if (tid == r && r < rows)
+            part_lse[(size_t)w.slot + r] = sum > 0.f ? m[r] + __log2f(sum) : -INFINITY;
     }
     return true;
 }
@@ -1219,6 +1254,7 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         tma_prefetch_desc(&tmV);
     }
     make_plan<PAGED>(p, tab, reinterpret_cast<int *>(smem), sh.scan);
+    launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1258,16 +1294,17 @@ shared_combine_kernel(const Params p, uint16_t *__restrict__ o, float *__restric
     const long long at = (long long)blockIdx.x * kCombineWarps + warp_id();
     if (at >= (long long)tokens * p.Hq) return;
     const int tok = (int)(at / p.Hq), h = (int)(at % p.Hq), kvh = h / p.G;
+    wait_for_launcher();
     // up to two runs of partials: first row, number, rows apart
     int base[2] = {0, 0}, num[2] = {0, 0}, apart[2] = {0, 0};
     auto take = [&](int k, int item, int row) {
-        const int4 t = __ldg(p.items + item);
+        const int4 t = __ldcg(p.items + item);
         base[k] = t.x + row;
         num[k] = t.y;
         apart[k] = t.z;
     };
     if constexpr (PAGED) {
-        const int4 s = __ldg(p.seqs + tok);
+        const int4 s = __ldcg(p.seqs + tok);
         take(0, s.x, h % p.G);
         if (s.y >= 0) {
             const int row = (tok - s.z) * p.G + h % p.G;
@@ -1286,7 +1323,7 @@ shared_combine_kernel(const Params p, uint16_t *__restrict__ o, float *__restric
     };
     const float z = sinks ? __ldg(sinks + h) * 1.4426950408889634f : -INFINITY;
     float m = z;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldg(pl + row_of(i)));
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(pl + row_of(i)));
     #pragma unroll
     for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float acc[PER], sum = 0.f;
@@ -1297,16 +1334,16 @@ shared_combine_kernel(const Params p, uint16_t *__restrict__ o, float *__restric
         #pragma unroll 4
         for (int i = 0; i < n; ++i) {
             const size_t rr = row_of(i);
-            const float wgt = ex2(__ldg(pl + rr) - m);
+            const float wgt = ex2(__ldcg(pl + rr) - m);
             sum += wgt;
             if constexpr (PER == 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(po + rr * D));
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + rr * D));
                 acc[0] = fmaf(wgt, v.x, acc[0]);
                 acc[1] = fmaf(wgt, v.y, acc[1]);
                 acc[2] = fmaf(wgt, v.z, acc[2]);
                 acc[3] = fmaf(wgt, v.w, acc[3]);
             } else {
-                const float2 v = __ldg(reinterpret_cast<const float2 *>(po + rr * D));
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(po + rr * D));
                 acc[0] = fmaf(wgt, v.x, acc[0]);
                 acc[1] = fmaf(wgt, v.y, acc[1]);
             }
@@ -1357,17 +1394,33 @@ int launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, const 
     using C = Cfg<D>;
     constexpr int smem = C::kOffTable + (int)sizeof(Table) + 1024;
     static_assert(smem + sizeof(Shared) <= 232448, "shared memory");
-    if (cudaFuncSetAttribute(shared_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess)
-        return -5;
+    // once per device: the attribute stays
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -5;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(shared_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 smem) != cudaSuccess)
+            return -5;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     shared_kernel<D, PAGED><<<p.n * p.Hkv, kThreads, smem, stream>>>(tk, tv, p);
     if (cudaGetLastError() != cudaSuccess) return -5;
+    // The combine is set up while the main kernel's last CTAs run.
     const int tokens = p.S * p.Nq;
     const long long rows = (long long)tokens * p.Hq;
-    shared_combine_kernel<D, PAGED>
-        <<<(unsigned)((rows + kCombineWarps - 1) / kCombineWarps), 32 * kCombineWarps, 0, stream>>>(
-            p, static_cast<uint16_t *>(a.o), a.lse, a.sinks, tokens);
-    return cudaGetLastError() == cudaSuccess ? 0 : -5;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((rows + kCombineWarps - 1) / kCombineWarps));
+    cfg.blockDim = dim3(32 * kCombineWarps);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, shared_combine_kernel<D, PAGED>, p, static_cast<uint16_t *>(a.o),
+                              a.lse, a.sinks, tokens) == cudaSuccess ? 0 : -5;
 }
 
 int launch_any(const SharedArgs &a, cudaStream_t stream) {
