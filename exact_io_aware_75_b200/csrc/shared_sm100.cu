@@ -23,9 +23,9 @@
 //     gives one partial (fp32 O, LSE) per row and item it touches.  The plan
 //     (prefix sums over the items) is computed by every CTA for itself in
 //     shared memory, about two microseconds; lengths never come to the host.
-//   * Warp 8 feeds a ring of K and V tiles (128 keys) by TMA, page by page
-//     through the block table, and runs ahead over the items.  Warp 10 clears
-//     the V rows behind a sequence's end (they may hold anything, and P = 0
+//   * Warps 8 and 10 feed a ring of K and V tiles (128 keys) by TMA, page by
+//     page through the block table, and run ahead over the items.  V rows
+//     behind a sequence's end are cleared (they may hold anything, and P = 0
 //     times NaN is NaN).
 //   * Up to 32 rows (a sequence's own pages, a token against its encoder
 //     states): S^T = K Q^T and O^T += V^T P^T, so that the keys (then the head
@@ -60,7 +60,7 @@ constexpr int kBlockN = 128;        // keys per K/V tile
 constexpr int kPagesPerBlock = kBlockN / kPage;
 constexpr int kRows = 2 * kBlockM;  // rows per item
 constexpr int kThreads = 384;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpClear = 10, kWarpMmaPV = 11;
+constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10;   // and 11: P V of few rows
 // Registers: launched with 384 x 168; softmax warpgroups 216, the rest 72
 // (2 * 128 * 216 + 128 * 72 = 64,512).
 constexpr int kRegsSoftmax = 216, kRegsControl = 72;
@@ -120,7 +120,7 @@ struct Params {
 
 struct Shared {
     uint64_t q_full[2];
-    uint64_t kv_full[8], kv_empty[8], tail[8];
+    uint64_t kv_full[8], kv_empty[8], tail;
     uint64_t s_full[2], p_lo[2], p_hi[2], o_full[2];
     uint64_t st_full[2][kSBufs], st_empty[2][kSBufs], pt_full[2][2], pt_empty[2][2];
     uint64_t drain[2];
@@ -427,14 +427,37 @@ __device__ __forceinline__ bool needs_clear(const Params &p, const Work &w, int 
     return (long long)w.it.src * p.Nk + w.it.keys < p.total_k;
 }
 
-// ------------------------------------------------------------- TMA producer
-template <int D, bool PAGED>
-__device__ void producer(const CUtensorMap *tmK, const CUtensorMap *tmV, const Params &p,
-                         const Table &tab, Shared &sh, uint8_t *sKV) {
+// ------------------------------------------------------------ TMA producers
+// Warp 8 fetches K tiles, warp 10 V tiles: a paged tile is 16 (d = 128) small
+// copies, some 1,300 cycles to issue, and one warp for both would need the
+// whole time in which a block crosses HBM.
+// A V tile in which the item's keys end counts its bytes on a barrier of its
+// own; the warp waits for them, writes zeros behind the keys and only then
+// completes the slot.  It does so after the next tile's copies, or before it
+// waits for a slot: the slot may need this very tile.
+template <int D, bool PAGED, bool V>
+__device__ void producer(const CUtensorMap *tm, const Params &p, const Table &tab, Shared &sh,
+                         uint8_t *sKV) {
     using C = Cfg<D>;
     volatile int *abort = &sh.abort;
     const int lane = lane_id(), kvh = blockIdx.x % p.Hkv;
-    uint32_t it = 0, tail_last = 0, tail_phase = 0;
+    uint32_t it = V ? 1 : 0;
+    int pending = -1, pending_valid = 0;      // slot of a tile to clear
+    uint32_t tail_phase = 0;
+    auto clear = [&]() -> bool {
+        if (!mbar_wait_warp(&sh.tail, tail_phase & 1, abort)) return false;
+        ++tail_phase;
+        uint8_t *dst = sKV + pending * C::kTileBytes + pending_valid * 128;
+        const int words = (kBlockN - pending_valid) * 8;
+        for (int b = 0; b < C::kBoxes; ++b)
+            for (int i = lane; i < words; i += 32)
+                *reinterpret_cast<uint4 *>(dst + b * C::kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kv_full[pending]);
+        pending = -1;
+        return true;
+    };
     Walker walk;
     walk.begin(p, tab);
     Work w;
@@ -446,7 +469,7 @@ __device__ void producer(const CUtensorMap *tmK, const CUtensorMap *tmV, const P
             return __ldg(p.block_table + (size_t)w.it.src * p.max_pages + w.it.page0 + c);
         };
         int ahead = page_of(w.kb0);
-        for (int j = w.kb0; j < w.kb1; ++j) {
+        for (int j = w.kb0; j < w.kb1; ++j, it += 2) {
             int page = ahead;
             ahead = page_of(j + 1);
             const int valid = w.it.keys - j * kBlockN;
@@ -455,69 +478,47 @@ __device__ void producer(const CUtensorMap *tmK, const CUtensorMap *tmV, const P
                 report_error(kDevErrInput);
                 page = 0;
             }
-            const bool clear = needs_clear<PAGED>(p, w, valid);
-            for (int kv = 0; kv < 2; ++kv, ++it) {
-                const int slot = it % C::kStages;
-                const uint32_t bit = 1u << slot;
-                uint8_t *dst = sKV + slot * C::kTileBytes;
-                if (!mbar_wait_warp(&sh.kv_empty[slot], ((it / C::kStages) & 1) ^ 1, abort)) goto out;
-                const bool tail = kv == 1 && clear;
-                uint64_t *bar = tail ? &sh.tail[slot] : &sh.kv_full[slot];
-                tail_last = tail ? tail_last | bit : tail_last & ~bit;
-                if (tail) tail_phase ^= bit;
-                if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
-                __syncwarp();
-                if (PAGED) {
-                    if (lane < kPagesPerBlock) {
-                        // (rows past the cache's extent arrive as zeros)
-                        const int row = page >= 0 ? page * kPage : p.num_pages * kPage;
-                        for (int b = 0; b < C::kBoxes; ++b)
-                            tma_load_3d(dst + b * C::kBoxBytes + lane * kPage * 128, kv ? tmV : tmK,
-                                        bar, b * 64, kvh, row);
-                    }
-                } else if (lane < C::kBoxes) {
-                    tma_load_3d(dst + lane * C::kBoxBytes, kv ? tmV : tmK, bar, lane * 64, kvh,
-                                w.it.src * p.Nk + j * kBlockN);
+            const int slot = it % C::kStages;
+            const uint32_t parity = ((it / C::kStages) & 1) ^ 1;
+            uint8_t *dst = sKV + slot * C::kTileBytes;
+            if (V && pending >= 0 &&
+                !__all_sync(0xffffffffu, mbar_test(smem_u32(&sh.kv_empty[slot]), parity)) && !clear())
+                goto out;
+            if (!mbar_wait_warp(&sh.kv_empty[slot], parity, abort)) goto out;
+            const bool tail = V && needs_clear<PAGED>(p, w, valid);
+            if (V && tail && pending >= 0 && !clear()) goto out;     // one at a time
+            uint64_t *bar = tail ? &sh.tail : &sh.kv_full[slot];
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
+            __syncwarp();
+            if (PAGED) {
+                if (lane < kPagesPerBlock) {
+                    // (rows past the cache's extent arrive as zeros)
+                    const int row = page >= 0 ? page * kPage : p.num_pages * kPage;
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        tma_load_3d(dst + b * C::kBoxBytes + lane * kPage * 128, tm, bar, b * 64, kvh, row);
                 }
+            } else if (lane < C::kBoxes) {
+                tma_load_3d(dst + lane * C::kBoxBytes, tm, bar, lane * 64, kvh,
+                            w.it.src * p.Nk + j * kBlockN);
+            }
+            if (V && pending >= 0 && !clear()) {
+                it += 2;
+                goto out;
+            }
+            if (tail) {
+                pending = slot;
+                pending_valid = valid;
             }
         }
     }
+    if (V && pending >= 0) clear();
     return;
 out:
     // Leave no copy in flight: wait for the last load issued into each slot.
-    if (lane == 0)
-        for (int s = 0; s < C::kStages; ++s)
-            if (it > (uint32_t)s) {
-                if (tail_last >> s & 1)
-                    mbar_drain_wait(&sh.tail[s], (tail_phase >> s & 1) ^ 1);
-                else
-                    mbar_drain_wait(&sh.kv_full[s], ((it - 1 - s) / C::kStages) & 1);
-            }
-}
-
-// Warp 10: zeros over the V rows behind an item's last key.
-template <int D, bool PAGED>
-__device__ void clear_tails(const Params &p, const Table &tab, Shared &sh, uint8_t *sKV) {
-    using C = Cfg<D>;
-    const int lane = lane_id();
-    uint32_t phase = 0;
-    Walker walk;
-    walk.begin(p, tab);
-    Work w;
-    while (walk.next<PAGED>(p, tab, w)) {
-        const int valid = w.it.keys - (w.kb1 - 1) * kBlockN;
-        if (!needs_clear<PAGED>(p, w, valid)) continue;
-        const int slot = (w.ring + 2 * (w.kb1 - w.kb0) - 1) % C::kStages;   // the share's last V tile
-        if (!mbar_wait_warp(&sh.tail[slot], phase >> slot & 1, &sh.abort)) return;
-        phase ^= 1u << slot;
-        uint8_t *dst = sKV + slot * C::kTileBytes + valid * 128;
-        const int words = (kBlockN - valid) * 8;
-        for (int b = 0; b < C::kBoxes; ++b)
-            for (int i = lane; i < words; i += 32)
-                *reinterpret_cast<uint4 *>(dst + b * C::kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
+    if (lane == 0) {
+        if (pending >= 0) mbar_drain_wait(&sh.tail, tail_phase & 1);
+        for (uint32_t s = V ? 1 : 0; s < C::kStages; s += 2)
+            if (it > s && (int)s != pending) mbar_drain_wait(&sh.kv_full[s], ((it - 2 - s) / C::kStages) & 1);
     }
 }
 
@@ -1243,16 +1244,14 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&sh.kv_full[s], 1);
             mbar_init(&sh.kv_empty[s], s & 1 ? 1 : 2);   // V: a commit; K: two softmax warps
-            mbar_init(&sh.tail[s], 1);
         }
+        mbar_init(&sh.tail, 1);
         sh.abort = 0;
         fence_barrier_init();
     }
     if (warp == kWarpMma) tmem_alloc(&sh.tmem_base, kTmemCols);
-    if (warp == kWarpTma && lane_id() == 0) {
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-    }
+    if (warp == kWarpK && lane_id() == 0) tma_prefetch_desc(&tmK);
+    if (warp == kWarpV && lane_id() == 0) tma_prefetch_desc(&tmV);
     make_plan<PAGED>(p, tab, reinterpret_cast<int *>(smem), sh.scan);
     launch_dependents();
     tc_fence_before();
@@ -1263,10 +1262,10 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         softmax_wg<D, PAGED>(p, tab, sh, smem);
     } else {
         regs_decrease<kRegsControl>();
-        if (warp == kWarpTma)
-            producer<D, PAGED>(&tmK, &tmV, p, tab, sh, sKV);
-        else if (warp == kWarpClear)
-            clear_tails<D, PAGED>(p, tab, sh, sKV);
+        if (warp == kWarpK)
+            producer<D, PAGED, false>(&tmK, p, tab, sh, sKV);
+        else if (warp == kWarpV)
+            producer<D, PAGED, true>(&tmV, p, tab, sh, sKV);
         else if (warp == kWarpMma)
             mma_issuer<D, PAGED>(p, tab, sh, smem, sKV);
         else
