@@ -924,7 +924,7 @@ bool cross_fits(int Hq, int Hkv, int Nq, int Nk) {
     const int G = Hq / Hkv;
     const long long rows = (long long)Nq * G;
     return G <= kSharedMaxGroup && rows <= 256ll * fa::kSharedMaxItems &&
-           fa::kSharedMaxItems * 4ll * (Nk / 128 + 2) <= INT32_MAX / 2;
+           fa::kSharedMaxItems * 8ll * (Nk / 128 + 2) <= INT32_MAX / 2;
 }
 
 }  // namespace
@@ -957,10 +957,10 @@ int fa_decode_shared(const void *q, const void *k_cache, const void *v_cache,
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o ||
         (num_groups > 0 && (!cu_groups || !prefix_lens)))
         return FA_ERR_INVALID_ARG;
-    // 32-bit row coordinates, page counts and plan costs (at most 3 per block of 8 pages and item)
+    // 32-bit row coordinates, page counts and plan costs (at most 8 per block of 8 pages, 5 per item)
     const long long items = 2ll * num_seqs + (long long)num_seqs * G / 256 + 1;
     if ((long long)num_pages * page_size > INT32_MAX / 2 || max_pages_per_seq >= 1 << 22 ||
-        items * 4 * (max_pages_per_seq / 8 + 2) > INT32_MAX / 2)
+        items * 8 * (max_pages_per_seq / 8 + 2) > INT32_MAX / 2)
         return FA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
         !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_groups) ||

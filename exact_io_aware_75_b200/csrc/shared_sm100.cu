@@ -73,9 +73,16 @@ constexpr int kMaxItems = kSharedMaxItems;
 static_assert(kMaxSeqs + kMaxGroupItems <= kMaxItems, "items of a paged batch");
 constexpr int kFewRows = 32;                // rows at most in the transposed form
 constexpr int kSBufs = 4;                   // S^T buffers per warpgroup, 32 columns each
-// Cost of a key block, in half tiles of K/V read from HBM, and of an item
-// besides (its first loads and its epilogue).
-constexpr int kCostBlock = 2, kCostBlock2 = 3, kCostItem = 1;
+// What a key block costs a CTA, by the item's rows, and an item besides (its
+// first loads and its epilogue).  Measured on prefixes of 131,072 tokens, 8 KV
+// heads, us per block: d = 128 1.31 (4 rows), 1.34 (128), 2.18 (256); d = 64
+// 0.80 (4), 0.76 (16), 1.00 (32), 1.17 (128), 2.18 (256).  Up to 128 rows at
+// d = 128 that is the rate of HBM, 7.0 to 7.2 TB/s.
+template <int D>
+struct Cost {
+    static constexpr int kFew = 3, kOne = D == 128 ? 3 : 4, kPair = D == 128 ? 5 : 8;
+};
+constexpr int kCostItem = 1, kCostBigItem = 5;
 
 template <int D>
 struct Cfg {
@@ -83,8 +90,8 @@ struct Cfg {
     static constexpr int kBoxBytes = kBlockM * 128;            // 128 rows x 128 bytes
     static constexpr int kTileBytes = kBlockM * D * 2;
     static constexpr int kStages = D == 128 ? 4 : 8;           // K in the even slots, V in the odd
-    // Q of a warpgroup's tile: 32 KB for either head dim.  With few rows: Q's
-    // rows at the start of each box, two buffers of P^T behind them.
+    // Q of a warpgroup's tile: 32 KB for either head dim.  With few rows: two
+    // buffers of Q and two of P^T.
     static constexpr int kQBytes = 32768;
     static constexpr int kOffKV = 2 * kQBytes;
     static constexpr int kOffTable = kOffKV + kStages * kTileBytes;
@@ -113,6 +120,7 @@ struct Params {
     int Hq, Hkv, G, Nq, Nk, pairs;
     uint32_t G_magic;
     int n;                     // CTAs per KV head
+    int cost_few, cost_one, cost_pair;
     int total_k;               // dense: stored key rows
     long long cap;
     float scale_log2;
@@ -133,8 +141,10 @@ struct Shared {
 // Rows of a P^T buffer (and N of the transposed products): 16 or 32.
 __device__ __forceinline__ int few_n(int rows) { return rows <= 16 ? 16 : 32; }
 
-// P^T buffer b of a warpgroup, within its Q tile.
+// Within a warpgroup's Q tile: P^T buffer b, and Q buffer b (its second box
+// one kBoxBytes on).
 __device__ __forceinline__ int few_p(int b) { return b ? 20480 : 4096; }
+__device__ __forceinline__ int few_q(int b) { return b * 12288; }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -159,20 +169,20 @@ struct Item {
 };
 
 template <bool PAGED>
-__device__ __forceinline__ Item get_item(const Params &p, const Table &tab, int i) {
+__device__ __forceinline__ Item get_item(const Params &p, const Table &tab, int groups, int i) {
     Item w;
     int all = p.Nq * p.G;
     w.row0 = 0;
     w.page0 = 0;
     if constexpr (PAGED) {
-        if (i < tab.num_group_items) {
+        if (i < groups) {
             const int g = tab.gi[i] & 0xffff, first = tab.cu[g];
             w.tok0 = w.src = first;
             all = (tab.cu[g + 1] - first) * p.G;
             w.row0 = (int)(tab.gi[i] >> 16) * kRows;
             w.keys = tab.own[first] * kPage;
         } else {
-            w.tok0 = w.src = i - tab.num_group_items;
+            w.tok0 = w.src = i - groups;
             w.page0 = tab.own[w.src];
             w.keys = tab.keys[w.src];
         }
@@ -186,28 +196,31 @@ __device__ __forceinline__ Item get_item(const Params &p, const Table &tab, int 
     return w;
 }
 
-template <bool PAGED>
-__device__ __forceinline__ Item item_of(const Params &p, const Table &tab, int i) {
-    return get_item<PAGED>(p, tab, i);
-}
-
 // x / G for the rows of a launch (G_magic = ceil(2^32 / G), exact as x * G < 2^32).
 __device__ __forceinline__ int div_group(const Params &p, int x) {
     return p.G == 1 ? x : (int)__umulhi((uint32_t)x, p.G_magic);
 }
 
-// ceil(x / cost) for the two costs, x < 2^30.
-__device__ __forceinline__ int div_cost(int x, int cost) {
-    return cost == kCostBlock ? (x + 1) >> 1 : (int)__umulhi((uint32_t)(x + 2), 0x55555556u);
+// ceil(x / c) for the costs, x < 2^30.
+__device__ __forceinline__ int div_cost(int x, int c) {
+    const uint32_t y = (uint32_t)(x + c - 1);
+    return (int)(c == 3 ? __umulhi(y, 0x55555556u) : c == 5 ? __umulhi(y, 0x33333334u)
+                 : c == 4 ? y >> 2 : y >> 3);
 }
-static_assert(kCostBlock == 2 && kCostBlock2 == 3, "div_cost");
 
-__device__ __forceinline__ int block_cost(int rows) { return rows > kBlockM ? kCostBlock2 : kCostBlock; }
+__device__ __forceinline__ int block_cost(const Params &p, int rows) {
+    return rows > kBlockM ? p.cost_pair : rows > 16 ? p.cost_one : p.cost_few;
+}
+__device__ __forceinline__ int item_cost(const Params &p, int rows, int keys) {
+    return keys > 0 ? ceil_div(keys, kBlockN) * block_cost(p, rows) + (rows > kFewRows ? kCostBigItem : kCostItem)
+                    : 0;
+}
 
-// The plan and the walk over the shares run once or a few times per CTA: what
-// they cost is fetching their instructions.  Their loops are not unrolled and
-// their parts are functions of their own, one copy for all warps (inlined and
-// unrolled, the plan took 3.5 us where it now takes FIXME).
+// x / span, 0 <= x < 2^31, given inv = floor((2^32 - 1) / span).
+__device__ __forceinline__ int div_span(int x, int span, uint32_t inv) {
+    const int q = (int)__umulhi((uint32_t)x, inv);
+    return x - q * span >= span ? q + 1 : q;
+}
 
 // Exclusive prefix sum over the block's threads; `total` gets the sum.
 __device__ __forceinline__ int block_scan(int x, int *s_warp, int &total) {
@@ -327,25 +340,30 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     int sum = 0, total;
     #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-        const Item w = item_of<PAGED>(p, tab, i);
+        const Item w = get_item<PAGED>(p, tab, ni, i);
         tab.start[i] = sum;
-        if (w.keys > 0) sum += ceil_div(w.keys, kBlockN) * block_cost(w.rows) + kCostItem;
+        sum += item_cost(p, w.rows, w.keys);
     }
     const int before = block_scan(sum, s_warp, total);
-    // (every share must hold the start of a block of any item it lies inside)
-    const int span = max(kCostBlock2, ceil_div(total, p.n));
+    // (every share must hold the start of a block of any item it lies inside:
+    // no block costs more than a share; only batches of more than 128 rows can
+    // have the dearest kind)
+    const int most = p.S * p.Nq * p.G > kBlockM ? p.cost_pair : p.cost_one;
+    const int span = max(most, ceil_div(total, p.n));
+    const uint32_t inv = 0xffffffffu / (uint32_t)span;
     int rows = 0;
     #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-        const Item w = item_of<PAGED>(p, tab, i);
+        const Item w = get_item<PAGED>(p, tab, ni, i);
         const int start = tab.start[i] + before;
         tab.start[i] = start;
         int parts = 0;
         if (w.keys > 0) {
-            const int last = start + (ceil_div(w.keys, kBlockN) - 1) * block_cost(w.rows);
-            parts = last / span - start / span + 1;
+            const int last = start + (ceil_div(w.keys, kBlockN) - 1) * block_cost(p, w.rows);
+            parts = div_span(last, span, inv) - div_span(start, span, inv) + 1;
         }
         tab.slot[i] = rows;
+        if (lead) p.items[i] = make_int4(0, parts, w.rows, 0);
         rows += parts * w.rows;
     }
     int all;
@@ -353,11 +371,7 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         tab.slot[i] += slot0;
-        if (lead) {
-            const Item w = item_of<PAGED>(p, tab, i);
-            const int next = i + 1 < i1 ? tab.slot[i + 1] + slot0 : slot0 + rows;
-            p.items[i] = make_int4(tab.slot[i], (next - tab.slot[i]) / w.rows, w.rows, 0);
-        }
+        if (lead) p.items[i].x = tab.slot[i];
     }
     if (tid == 0) tab.span = span;
     __syncthreads();
@@ -376,55 +390,62 @@ struct Work {
 };
 
 struct Walker {
-    int i, lo, hi, share, turn;
+    int i, lo, hi, items, groups, part, turn;   // part: of the first item, whose blocks may begin before lo
     uint32_t ring;
     __device__ __forceinline__ void begin(const Params &p, const Table &tab) {
+        const int share = blockIdx.x / p.Hkv, span = tab.span;
         turn = 0;
         ring = 0;
-        share = blockIdx.x / p.Hkv;
-        lo = share * tab.span;
-        hi = lo + tab.span;
-        int a = 0, b = tab.num_items;          // the last item that starts at or before lo
+        items = tab.num_items;
+        groups = tab.num_group_items;
+        lo = share * span;
+        hi = lo + span;
+        int a = 0, b = items;                  // the last item that starts at or before lo
         #pragma unroll 1
         while (b - a > 1) {
             const int mid = (a + b) >> 1;
             if (tab.start[mid] <= lo) a = mid; else b = mid;
         }
         i = a;
+        part = share - tab.start[a] / span;
     }
     template <bool PAGED>
     __device__ __forceinline__ bool next(const Params &p, const Table &tab, Work &w) {
+        bool found = false;
         #pragma unroll 1
-        for (; i < tab.num_items; ++i) {
+        while (!found && i < items) {
+            // (the compiler must not carry the table's values from turn to turn:
+            // without this a build skipped every item after an empty one)
+            asm volatile("" ::: "memory");
             const int start = tab.start[i];
-            if (start >= hi) return false;
-            w.it = get_item<PAGED>(p, tab, i);
-            const int cost = block_cost(w.it.rows), nb = ceil_div(w.it.keys, kBlockN);
+            if (start >= hi) break;
+            w.it = get_item<PAGED>(p, tab, groups, i);
+            const int cost = block_cost(p, w.it.rows), nb = ceil_div(w.it.keys, kBlockN);
             w.kb0 = start >= lo ? 0 : min(nb, div_cost(lo - start, cost));
             w.kb1 = min(nb, div_cost(hi - start, cost));
-            if (w.kb0 >= w.kb1) continue;
-            w.pair = w.it.rows > kBlockM;
-            w.few = w.it.rows <= kFewRows;
-            w.wg = turn;
-            if (w.few) turn ^= 1;
-            w.rep = w.it.rows > 64 ? 1 : 2;
-            w.ring = ring;
-            ring += 2 * (w.kb1 - w.kb0);
-            w.slot = tab.slot[i] + (start >= lo ? 0 : share - start / tab.span) * w.it.rows;
+            w.slot = tab.slot[i] + part * w.it.rows;
+            found = w.kb0 < w.kb1;
             ++i;
-            return true;
+            part = 0;
         }
-        return false;
+        if (!found) return false;
+        w.pair = w.it.rows > kBlockM;
+        w.few = w.it.rows <= kFewRows;
+        w.wg = turn;
+        if (w.few) turn ^= 1;
+        w.rep = w.it.rows > 64 ? 1 : 2;
+        w.ring = ring;
+        ring += 2 * (w.kb1 - w.kb0);
+        return true;
     }
 };
 
-// V rows behind the item's last key that the copy into shared memory brought:
-// of a page the keys end inside, or (dense) of whatever lies behind.
+// Whether V rows behind the item's last key have to be cleared: what the slot
+// or the page held (paged), what lies behind the sequence (dense; rows past the
+// tensor arrive as zeros).
 template <bool PAGED>
 __device__ __forceinline__ bool needs_clear(const Params &p, const Work &w, int valid) {
-    if (valid >= kBlockN) return false;
-    if (PAGED) return valid % kPage != 0;
-    return (long long)w.it.src * p.Nk + w.it.keys < p.total_k;
+    return valid < kBlockN && (PAGED || (long long)w.it.src * p.Nk + w.it.keys < p.total_k);
 }
 
 // ------------------------------------------------------------ TMA producers
@@ -458,57 +479,73 @@ __device__ void producer(const CUtensorMap *tm, const Params &p, const Table &ta
         pending = -1;
         return true;
     };
+    // lane i < 8: page i of a block (-1: behind the keys)
+    auto page_of = [&](const Work &w, int j) -> int {
+        const int c = j * kPagesPerBlock + lane;
+        if (!PAGED || lane >= kPagesPerBlock || c * kPage >= w.it.keys) return -1;
+        return __ldg(p.block_table + (size_t)w.it.src * p.max_pages + w.it.page0 + c);
+    };
     Walker walk;
     walk.begin(p, tab);
-    Work w;
-    while (walk.next<PAGED>(p, tab, w)) {
-        // lane i < 8: page i of a block (-1: behind the keys)
-        auto page_of = [&](int j) -> int {
-            const int c = j * kPagesPerBlock + lane;
-            if (!PAGED || lane >= kPagesPerBlock || j >= w.kb1 || c * kPage >= w.it.keys) return -1;
-            return __ldg(p.block_table + (size_t)w.it.src * p.max_pages + w.it.page0 + c);
-        };
-        int ahead = page_of(w.kb0);
-        for (int j = w.kb0; j < w.kb1; ++j, it += 2) {
-            int page = ahead;
-            ahead = page_of(j + 1);
-            const int valid = w.it.keys - j * kBlockN;
-            if (PAGED && lane < kPagesPerBlock && lane * kPage < valid &&
-                (page < 0 || page >= p.num_pages)) {
-                report_error(kDevErrInput);
-                page = 0;
-            }
-            const int slot = it % C::kStages;
-            const uint32_t parity = ((it / C::kStages) & 1) ^ 1;
-            uint8_t *dst = sKV + slot * C::kTileBytes;
-            if (V && pending >= 0 &&
-                !__all_sync(0xffffffffu, mbar_test(smem_u32(&sh.kv_empty[slot]), parity)) && !clear())
-                goto out;
-            if (!mbar_wait_warp(&sh.kv_empty[slot], parity, abort)) goto out;
-            const bool tail = V && needs_clear<PAGED>(p, w, valid);
-            if (V && tail && pending >= 0 && !clear()) goto out;     // one at a time
-            uint64_t *bar = tail ? &sh.tail : &sh.kv_full[slot];
-            if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
-            __syncwarp();
-            if (PAGED) {
-                if (lane < kPagesPerBlock) {
-                    // (rows past the cache's extent arrive as zeros)
-                    const int row = page >= 0 ? page * kPage : p.num_pages * kPage;
-                    for (int b = 0; b < C::kBoxes; ++b)
-                        tma_load_3d(dst + b * C::kBoxBytes + lane * kPage * 128, tm, bar, b * 64, kvh, row);
-                }
-            } else if (lane < C::kBoxes) {
-                tma_load_3d(dst + lane * C::kBoxBytes, tm, bar, lane * 64, kvh,
-                            w.it.src * p.Nk + j * kBlockN);
-            }
-            if (V && pending >= 0 && !clear()) {
-                it += 2;
-                goto out;
-            }
-            if (tail) {
-                pending = slot;
-                pending_valid = valid;
-            }
+    Work w, after;
+    bool have = walk.next<PAGED>(p, tab, w);
+    int j = 0, ahead = -1;
+    if (have) {
+        j = w.kb0;
+        ahead = page_of(w, j);
+    }
+    while (have) {
+        // the pages of the block after this one, of whatever share, are looked
+        // up while this one's copies go out
+        int page = ahead;
+        const bool last = j + 1 == w.kb1;
+        if (last) {
+            have = walk.next<PAGED>(p, tab, after);
+            if (have) ahead = page_of(after, after.kb0);
+        } else {
+            ahead = page_of(w, j + 1);
+        }
+        const int valid = w.it.keys - j * kBlockN;
+        const int pages = PAGED ? min(kPagesPerBlock, ceil_div(valid, kPage)) : 0;
+        if (PAGED && lane < pages && (page < 0 || page >= p.num_pages)) {
+            report_error(kDevErrInput);
+            page = 0;
+        }
+        const int slot = it % C::kStages;
+        const uint32_t parity = ((it / C::kStages) & 1) ^ 1;
+        uint8_t *dst = sKV + slot * C::kTileBytes;
+        if (V && pending >= 0 &&
+            !__all_sync(0xffffffffu, mbar_test(smem_u32(&sh.kv_empty[slot]), parity)) && !clear())
+            goto out;
+        if (!mbar_wait_warp(&sh.kv_empty[slot], parity, abort)) goto out;
+        const bool tail = V && needs_clear<PAGED>(p, w, valid);
+        if (V && tail && pending >= 0 && !clear()) goto out;     // one at a time
+        uint64_t *bar = tail ? &sh.tail : &sh.kv_full[slot];
+        if (lane == 0)
+            mbar_arrive_expect_tx(bar, PAGED ? pages * kPage * D * 2 : C::kTileBytes);
+        __syncwarp();
+        if (PAGED) {
+            if (lane < pages)
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(dst + b * C::kBoxBytes + lane * kPage * 128, tm, bar, b * 64, kvh,
+                                page * kPage);
+        } else if (lane < C::kBoxes) {
+            tma_load_3d(dst + lane * C::kBoxBytes, tm, bar, lane * 64, kvh,
+                        w.it.src * p.Nk + j * kBlockN);
+        }
+        if (V && pending >= 0 && !clear()) {
+            it += 2;
+            goto out;
+        }
+        if (tail) {
+            pending = slot;
+            pending_valid = valid;
+        }
+        it += 2;
+        ++j;
+        if (last && have) {
+            w = after;
+            j = w.kb0;
         }
     }
     if (V && pending >= 0) clear();
@@ -540,7 +577,7 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
     const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(sKV), 16);
     const uint32_t v_lo = desc_lo(smem_u32(sKV), C::kBoxBytes);
     constexpr uint32_t kTileStep = C::kTileBytes >> 4, kQStep = C::kQBytes >> 4;
-    uint32_t q_uses[2] = {0, 0}, p_cnt[2] = {0, 0}, st_cnt[2] = {0, 0};
+    uint32_t q_uses[2] = {0, 0}, p_cnt[2] = {0, 0}, st_cnt[2] = {0, 0}, fewq[2] = {0, 0};
     // S_t = Q_t K^T (K-major operands, 128-byte swizzle, 64 columns per box)
     auto issue_s = [&](int t, int slot) {
         if (elect_one()) {
@@ -586,7 +623,7 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
         if (w.few) {
             // S^T = K Q^T into the warpgroup's next free buffer
             const uint32_t id = idesc_bf16_f32(kBlockN, few_n(w.it.rows), false);
-            const uint32_t q = q_lo + w.wg * kQStep;
+            const uint32_t q = q_lo + w.wg * kQStep + (few_q(fewq[w.wg]++ & 1) >> 4);
             if (!mbar_wait_warp(&sh.q_full[w.wg], q_uses[w.wg] & 1, abort)) goto out;
             ++q_uses[w.wg];
             for (int j = 0; j < nb; ++j, it += 2) {
@@ -705,40 +742,6 @@ out:
 }
 
 // ---------------------------------------------------------------- softmax
-template <int NC>
-__device__ __forceinline__ float max_of(const float (&v)[NC]) {
-    float m[4] = {v[0], v[1], v[2], v[3]};
-    #pragma unroll
-    for (int i = 4; i + 7 < NC; i += 8) {
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = fmax3(m[e], v[i + e], v[i + 4 + e]);
-    }
-    #pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], v[NC - 4 + e]);
-    return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
-}
-
-// P = 2^(s*scale*log2e - m), packed to bf16 pairs (rounded to nearest: off by
-// at most 2^-8 relative, as in the prefill), and their fp32 sum.
-template <int NC>
-__device__ __forceinline__ float exp_of(const float (&v)[NC], float sl2, float m,
-                                        uint32_t (&pk)[NC / 2]) {
-    const uint64_t c2 = f2pack(sl2, sl2), nm2 = f2pack(-m, -m);
-    uint64_t a2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-    #pragma unroll
-    for (int c = 0; c < NC / 2; ++c) {
-        float x0, x1;
-        f2unpack(f2fma(f2pack(v[2 * c], v[2 * c + 1]), c2, nm2), x0, x1);
-        x0 = ex2(x0);
-        x1 = ex2(x1);
-        a2[c & 1] = f2add(a2[c & 1], f2pack(x0, x1));
-        pk[c] = pack_bf16(x0, x1);
-    }
-    float a, b;
-    f2unpack(f2add(a2[0], a2[1]), a, b);
-    return a + b;
-}
-
 // A thread's running softmax: reference maximum (log2 units) and sum.
 struct Row {
     float m, l;
@@ -770,92 +773,67 @@ __device__ __forceinline__ void update_max(Row &r, float m_blk, bool first, uint
     r.m = m_new;
 }
 
-// Keys [col0, col0 + NC) of the block of which `limit` keys are the item's.
-template <int D, int NC>
-__device__ __forceinline__ void soft_part(Row &r, int col0, int limit, bool first, float sl2,
-                                          uint32_t tS, uint32_t tO, uint32_t (&pk)[NC / 2]) {
-    float s[NC];
-    {
-        uint32_t raw[NC];
-        #pragma unroll
-        for (int c = 0; c < NC; c += 32) tmem_ld32(tS + col0 + c, raw + c);
-        tmem_wait_ld();
-        #pragma unroll
-        for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(raw[c]);
-    }
+// 64 scores of this thread's row, keys behind `limit` masked.
+__device__ __forceinline__ void load_scores(float (&s)[64], uint32_t tS, int col0, int limit) {
+    uint32_t raw[64];
+    tmem_ld32(tS + col0, raw);
+    tmem_ld32(tS + col0 + 32, raw + 32);
+    tmem_wait_ld();
+    #pragma unroll
+    for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(raw[c]);
     if (limit < kBlockN) {
         #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < 64; ++c)
             if (col0 + c >= limit) s[c] = -INFINITY;
     }
-    update_max<D>(r, max_of(s) * sl2, first, tO);
-    r.l += exp_of(s, sl2, r.m == -INFINITY ? 0.f : r.m, pk);
 }
 
-// The softmax of one block, by one warp.  P_t goes over S_t: keys 0-63 in
-// columns 0-31, keys 64-127 in columns 64-95.
+// The softmax of one block, by one warp: both halves of its keys, or one (the
+// row's other copy has the other).  P_t goes over S_t: keys 0-63 in columns
+// 0-31, keys 64-127 in columns 64-95.  Scores are read from tensor memory
+// twice, for the maximum and for P: that is cheaper than 128 registers, and a
+// loop over the halves keeps the code short.
 template <int D>
 __device__ __forceinline__ void soft_block(Row &r, int rep, int limit, bool first, float sl2,
                                            uint32_t tS, uint32_t tO, Shared &sh, int t) {
-    const int q4 = warp_id() & 3;
-    if (rep == 2) {
-        uint32_t pk[32], z[32];
-        soft_part<D, 64>(r, (q4 >> 1) * 64, limit, first, sl2, tS, tO, pk);
-        #pragma unroll
-        for (int i = 0; i < 32; ++i) z[i] = 0u;
-        tmem_st32(tS + (q4 >> 1) * 64, pk);
-        tmem_st32(tS + (1 - (q4 >> 1)) * 64, z);
-    } else {
-        float sA[64], sB[64];
-        {
-            uint32_t raw[64];
-            tmem_ld32(tS, raw);
-            tmem_ld32(tS + 32, raw + 32);
-            tmem_wait_ld();
-            #pragma unroll
-            for (int c = 0; c < 64; ++c) sA[c] = __uint_as_float(raw[c]);
-        }
-        uint32_t raw[64];
-        tmem_ld32(tS + 64, raw);
-        tmem_ld32(tS + 96, raw + 32);
-        if (limit < kBlockN) {
-            #pragma unroll
-            for (int c = 0; c < 64; ++c)
-                if (c >= limit) sA[c] = -INFINITY;
-        }
-        const float mA = max_of(sA);
-        tmem_wait_ld();
-        #pragma unroll
-        for (int c = 0; c < 64; ++c) sB[c] = (limit < kBlockN && c + 64 >= limit)
-                                                 ? -INFINITY : __uint_as_float(raw[c]);
-        update_max<D>(r, fmaxf(mA, max_of(sB)) * sl2, first, tO);
-        const float mb = r.m == -INFINITY ? 0.f : r.m;
+    const int lo = rep == 2 ? (warp_id() & 3) >> 1 : 0, hi = rep == 2 ? lo + 1 : 2;
+    float top = -INFINITY;
+    #pragma unroll 1
+    for (int h = lo; h < hi; ++h) {
+        float s[64];
+        load_scores(s, tS, h * 64, limit);
+        top = fmaxf(top, prefill_impl::row_max64(s));
+    }
+    update_max<D>(r, top * sl2, first, tO);
+    const float mb = r.m == -INFINITY ? 0.f : r.m;
+    uint64_t acc = f2pack(0.f, 0.f);
+    #pragma unroll 1
+    for (int h = lo; h < hi; ++h) {
+        float s[64];
+        load_scores(s, tS, h * 64, limit);
         uint32_t pk[32];
-        uint64_t acc = f2pack(0.f, 0.f);
-        prefill_impl::exp_half(sA, sl2, mb, pk, acc);
-        tmem_st32(tS, pk);
+        prefill_impl::exp_half(s, sl2, mb, pk, acc);
+        tmem_st32(tS + h * 64, pk);
+        if (rep == 2) {
+            #pragma unroll
+            for (int i = 0; i < 32; ++i) pk[i] = 0u;
+            tmem_st32(tS + (1 - h) * 64, pk);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane_id() == 0) mbar_arrive(&sh.p_lo[t]);
-        prefill_impl::exp_half(sB, sl2, mb, pk, acc);
-        tmem_st32(tS + 64, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane_id() == 0) mbar_arrive(&sh.p_hi[t]);
-        float a0, a1;
-        f2unpack(acc, a0, a1);
-        r.l += a0 + a1;
-        return;
+        if (lane_id() == 0) {
+            if (rep == 2) {
+                mbar_arrive(&sh.p_lo[t]);
+                mbar_arrive(&sh.p_hi[t]);
+            } else {
+                mbar_arrive(h ? &sh.p_hi[t] : &sh.p_lo[t]);
+            }
+        }
     }
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane_id() == 0) {
-        mbar_arrive(&sh.p_lo[t]);
-        mbar_arrive(&sh.p_hi[t]);
-    }
+    float a0, a1;
+    f2unpack(acc, a0, a1);
+    r.l += a0 + a1;
 }
 
 template <int N>
@@ -899,12 +877,35 @@ struct Count {
     uint32_t s, blocks, o;   // S and P barriers; transposed blocks; O barrier
 };
 
+// Q of a share of few rows into buffer b, by asynchronous copies (zeros behind
+// the rows), swizzled as TMA would; sent off once they have arrived.
+template <int D>
+__device__ __forceinline__ void fetch_few_q(const Params &p, const Item &it, int kvh, uint8_t *tile, int b) {
+    const int words = (it.rows <= 4 ? 4 : it.rows <= 8 ? 8 : it.rows <= 16 ? 16 : 32) * (D / 8);
+    #pragma unroll 1
+    for (int x = threadIdx.x & 127; x < words; x += 128) {
+        const int row = x / (D / 8), c = x % (D / 8);
+        const int at = it.row0 + min(row, it.rows - 1), tok = div_group(p, at);
+        const uint16_t *src =
+            p.q + ((size_t)(it.tok0 + tok) * p.Hq + kvh * p.G + at - tok * p.G) * D + c * 8;
+        copy_async16(tile + few_q(b) + (c >> 3) * Cfg<D>::kBoxBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                     src, row < it.rows);
+    }
+}
+__device__ __forceinline__ void send_few_q(uint64_t *full) {
+    copy_async_wait_all();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(full);
+}
+
 // A share of up to RN rows, by one warpgroup: thread = key (of S^T), then
 // head-dim index (of O^T).  The reference maxima are the same in all threads.
 // False: a wait ran out (in all threads of the warpgroup alike).
 template <int D, int RN>
-__device__ bool few_rows(const Params &p, const Work &w, Shared &sh, uint8_t *tile, int wg, int kvh,
-                         Count &cnt, float *part_o, float *part_lse) {
+__device__ bool few_rows(const Params &p, const Work &w, Shared &sh, uint8_t *tile, int wg, Count &cnt,
+                         float *part_o, float *part_lse) {
     using C = Cfg<D>;
     constexpr int N = RN <= 16 ? 16 : 32;
     const int warp = warp_id(), q4 = warp & 3, lane = lane_id(), tid = threadIdx.x & 127;
@@ -914,31 +915,6 @@ __device__ bool few_rows(const Params &p, const Work &w, Shared &sh, uint8_t *ti
     const uint32_t tO = sh.tmem_base + lanes + C::kColO + wg * D;
     const int rows = w.it.rows;
     float *red = reinterpret_cast<float *>(&sh.ml[0][0]) + wg * 256;   // [4 warps][32] of this warpgroup
-    {
-        constexpr int kWords = RN * D / 8, kPer = (kWords + 127) / 128;
-        uint4 qv[kPer];
-        #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int x = tid + i * 128, row = x / (D / 8), c = x % (D / 8);
-            qv[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows) {
-                const int at = w.it.row0 + row, tok = div_group(p, at);
-                qv[i] = __ldg(reinterpret_cast<const uint4 *>(
-                    p.q + ((size_t)(w.it.tok0 + tok) * p.Hq + kvh * p.G + at - tok * p.G) * D) + c);
-            }
-        }
-        #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int x = tid + i * 128, row = x / (D / 8), c = x % (D / 8);
-            if (x < kWords)
-                *reinterpret_cast<uint4 *>(tile + (c >> 3) * C::kBoxBytes + row * 128 +
-                                           (((c & 7) ^ (row & 7)) << 4)) = qv[i];
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full[wg]);
-    }
     // (a finite start: no score is below it but -inf, whose P is 0 either way)
     constexpr float kLowest = -3.0e38f;
     float m[RN], l[RN];
@@ -1070,18 +1046,34 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
     Count cnt{0, 0, 0};
     Walker walk;
     walk.begin(p, tab);
-    Work w;
-    bool alive = true;
-    while (walk.next<PAGED>(p, tab, w)) {
+    Work w, after;
+    // the next share that is this warpgroup's
+    auto next = [&](Work &w) -> bool {
+        while (walk.next<PAGED>(p, tab, w))
+            if (!w.few || w.wg == t) return true;
+        return false;
+    };
+    uint8_t *tile = sQ + t * C::kQBytes;
+    uint32_t fewq = 0;
+    bool alive = true, have = next(w), fetched = false;
+    for (; have; w = after) {
         if (w.few) {
-            if (w.wg != t || !alive) continue;
-            uint8_t *tile = sQ + t * C::kQBytes;
-            alive = w.it.rows <= 4    ? few_rows<D, 4>(p, w, sh, tile, t, kvh, cnt, part_o, part_lse)
-                    : w.it.rows <= 8  ? few_rows<D, 8>(p, w, sh, tile, t, kvh, cnt, part_o, part_lse)
-                    : w.it.rows <= 16 ? few_rows<D, 16>(p, w, sh, tile, t, kvh, cnt, part_o, part_lse)
-                                      : few_rows<D, 32>(p, w, sh, tile, t, kvh, cnt, part_o, part_lse);
+            // Q of the next share is under way while this one is worked on
+            if (!fetched) fetch_few_q<D>(p, w.it, kvh, tile, fewq & 1);
+            if (alive) send_few_q(&sh.q_full[t]);
+            ++fewq;
+            have = next(after);
+            fetched = have && after.few;
+            if (fetched) fetch_few_q<D>(p, after.it, kvh, tile, fewq & 1);
+            if (!alive) continue;
+            alive = w.it.rows <= 4    ? few_rows<D, 4>(p, w, sh, tile, t, cnt, part_o, part_lse)
+                    : w.it.rows <= 8  ? few_rows<D, 8>(p, w, sh, tile, t, cnt, part_o, part_lse)
+                    : w.it.rows <= 16 ? few_rows<D, 16>(p, w, sh, tile, t, cnt, part_o, part_lse)
+                                      : few_rows<D, 32>(p, w, sh, tile, t, cnt, part_o, part_lse);
             continue;
         }
+        have = next(after);
+        fetched = false;
         if (!alive) {
             // (this warpgroup gave up: the other one must not wait for it below)
             named_bar_and(1, 256, false);
@@ -1104,7 +1096,7 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
             #pragma unroll
             for (int c = 0; c < D / 8; ++c)
                 qv[c] = lr < nrows ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-            uint8_t *dst = sQ + t * C::kQBytes + r * 128;
+            uint8_t *dst = tile + r * 128;
             #pragma unroll
             for (int c = 0; c < D / 8; ++c)
                 *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBoxBytes + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
@@ -1454,6 +1446,9 @@ int launch_any(const SharedArgs &a, cudaStream_t stream) {
     p.n = a.Hkv >= sms ? 1 : sms / a.Hkv;
     p.total_k = a.paged ? 0 : a.S_all * a.Nk;
     p.cap = part_rows(rows, a.Hkv, a.paged);
+    p.cost_few = a.d == 128 ? Cost<128>::kFew : Cost<64>::kFew;
+    p.cost_one = a.d == 128 ? Cost<128>::kOne : Cost<64>::kOne;
+    p.cost_pair = a.d == 128 ? Cost<128>::kPair : Cost<64>::kPair;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     // K/V rows: the cache's slots, read a page box at a time, or the sequences' stored keys
     alignas(64) CUtensorMap tk, tv;

@@ -210,6 +210,15 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// 16 bytes from global to shared memory, asynchronously (zeros if !valid).
+__device__ __forceinline__ void copy_async16(void *dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Programmatic dependent launch: lets the next kernel of the stream be set up
 // while this one runs; the other waits until this one and its writes are done.
 __device__ __forceinline__ void launch_dependents() {
