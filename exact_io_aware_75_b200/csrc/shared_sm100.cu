@@ -1273,17 +1273,21 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------- combine
-// One warp per (token, query head): the partials of the row's items.
+// The partials of one (token, query head) row, by SPLIT of a block's eight
+// warps: eight where there are few rows and so many partials each, else one
+// (32 rows of 18 partials: 11 us after the main kernel with one, FIXME with eight).
 constexpr int kCombineWarps = 8;
+constexpr int kCombineFewRows = 1024;
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int SPLIT>
 __global__ void __launch_bounds__(32 * kCombineWarps)
 shared_combine_kernel(const Params p, uint16_t *__restrict__ o, float *__restrict__ lse,
                       const float *__restrict__ sinks, int tokens) {
     constexpr int PER = D / 32;
-    const int lane = lane_id();
-    const long long at = (long long)blockIdx.x * kCombineWarps + warp_id();
-    if (at >= (long long)tokens * p.Hq) return;
+    __shared__ float s_acc[SPLIT > 1 ? kCombineWarps : 1][D + 1];
+    const int lane = lane_id(), part = warp_id() % SPLIT;
+    const long long at = (long long)blockIdx.x * (kCombineWarps / SPLIT) + warp_id() / SPLIT;
+    if (at >= (long long)tokens * p.Hq) return;      // (SPLIT = 8: the whole block or none)
     const int tok = (int)(at / p.Hq), h = (int)(at % p.Hq), kvh = h / p.G;
     wait_for_launcher();
     // up to two runs of partials: first row, number, rows apart
@@ -1321,9 +1325,9 @@ shared_combine_kernel(const Params p, uint16_t *__restrict__ o, float *__restric
     #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
     if (m != -INFINITY) {
-        sum = ex2(z - m);
+        if (part == 0) sum = ex2(z - m);
         #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
+        for (int i = part; i < n; i += SPLIT) {
             const size_t rr = row_of(i);
             const float wgt = ex2(__ldcg(pl + rr) - m);
             sum += wgt;
@@ -1338,6 +1342,20 @@ shared_combine_kernel(const Params p, uint16_t *__restrict__ o, float *__restric
                 acc[0] = fmaf(wgt, v.x, acc[0]);
                 acc[1] = fmaf(wgt, v.y, acc[1]);
             }
+        }
+    }
+    if constexpr (SPLIT > 1) {
+        static_assert(SPLIT == kCombineWarps, "one row per block");
+        #pragma unroll
+        for (int e = 0; e < PER; ++e) s_acc[part][lane * PER + e] = acc[e];
+        if (lane == 0) s_acc[part][D] = sum;
+        __syncthreads();
+        if (part > 0) return;
+        #pragma unroll
+        for (int k = 1; k < SPLIT; ++k) {
+            #pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] += s_acc[k][lane * PER + e];
+            sum += s_acc[k][D];
         }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -1405,13 +1423,17 @@ int launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, const 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((rows + kCombineWarps - 1) / kCombineWarps));
+    const bool few = rows <= kCombineFewRows;
+    const int per = few ? 1 : kCombineWarps;
+    cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
     cfg.blockDim = dim3(32 * kCombineWarps);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, shared_combine_kernel<D, PAGED>, p, static_cast<uint16_t *>(a.o),
-                              a.lse, a.sinks, tokens) == cudaSuccess ? 0 : -5;
+    return cudaLaunchKernelEx(&cfg, few ? shared_combine_kernel<D, PAGED, kCombineWarps>
+                                        : shared_combine_kernel<D, PAGED, 1>,
+                              p, static_cast<uint16_t *>(a.o), a.lse, a.sinks, tokens) == cudaSuccess
+               ? 0 : -5;
 }
 
 int launch_any(const SharedArgs &a, cudaStream_t stream) {
