@@ -44,6 +44,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "balance.cuh"
 #include "fa_internal.h"
 #include "sm100.cuh"
 
@@ -90,7 +91,6 @@ constexpr int kDQBytes = kDQHalf * kD * 4;       // 16 KB staging buffer
 constexpr int kOffDQ = kOffDS + 2 * kDSBytes;    // two staging buffers
 constexpr int kOffRows = kOffDQ + 2 * kDQBytes;  // stage s: lse2[64], D[64] (fp32)
 constexpr int kSmemBytes = kOffRows + kStages * 2 * kBlockQ * 4 + 1024;
-static_assert(kSmemBytes + 256 <= 232448, "shared memory");
 constexpr int kBarDrain = 1;                     // named barrier of the dQ warps
 
 struct Params {
@@ -117,20 +117,76 @@ struct Unit {
     int t_lo, nt;      // query tiles [t_lo, t_lo + nt) of each query head
     int ntiles;        // group * nt
     int tokk0, Lk;     // first key and visible keys (tok0 and L but for cross attention)
-    int Ls;            // cross attention: stored keys; those past Lk get zero gradients
+    // cross attention: stored keys; those past Lk get zero gradients, from the
+    // head's last unit
+    int Ls;
+    bool last;
 };
 
-// False if the unit has no (query, key) pair.  Cross attention: w.Ls is then
-// the number of key rows that still get zero gradients.
-template <bool CROSS>
-__device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
+// Cross attention: where a sequence's queries and keys lie (Ls: its stored
+// keys, of which Lk are visible); false if they do not fit.
+__device__ __forceinline__ bool cross_lengths(const Params &p, int s, int &tok0, int &L, int &tokk0,
+                                              int &Lk, int &Ls) {
+    if (p.cu_seqlens) {
+        tok0 = __ldg(p.cu_seqlens + s);
+        L = __ldg(p.cu_seqlens + s + 1) - tok0;
+        tokk0 = __ldg(p.cu_seqlens_k + s);
+        Ls = Lk = __ldg(p.cu_seqlens_k + s + 1) - tokk0;
+        return tok0 >= 0 && L >= 0 && L <= p.max_seqlen && tok0 <= p.total_tokens - L && tokk0 >= 0 &&
+               Lk >= 0 && Lk <= p.max_seqlen_k && tokk0 <= p.total_k - Lk;
+    }
+    tok0 = s * p.seqlen;
+    L = p.seqlen;
+    tokk0 = s * p.seqlen_k;
+    Ls = p.seqlen_k;
+    Lk = p.seq_lens_k ? __ldg(p.seq_lens_k + s) : p.seqlen_k;
+    return Lk >= 0 && Lk <= p.seqlen_k;
+}
+
+// What a KV head's units of a sequence cost, in query tiles; a unit's K and V
+// and its dK and dV count as four.  The last unit also clears the gradients of
+// keys that no query sees; a sequence without any (query, key) pair has one
+// unit for that.
+struct CrossCost {
+    const Params &p;
+    __device__ __forceinline__ SeqCost operator()(int s, bool report) const {
+        int tok0, L, tokk0, Lk, Ls;
+        if (!cross_lengths(p, s, tok0, L, tokk0, Lk, Ls)) {
+            if (report && blockIdx.x == 0) report_error(kDevErrInput);
+            return SeqCost{0, 0, 0};
+        }
+        if (Ls == 0) return SeqCost{0, 0, 0};
+        if (L == 0 || Lk == 0) return SeqCost{1, 1 + Ls / kBlockK, 1 + Ls / kBlockK};
+        const int unit = p.group * ((L + kBlockQ - 1) / kBlockQ) + 4;
+        return SeqCost{(Lk + kBlockK - 1) / kBlockK, unit, unit};
+    }
+};
+
+// False if the unit has no (query, key) pair.
+template <bool CROSS, class U>
+__device__ __forceinline__ bool get_unit(const U &u_, const Params &p, Unit &w) {
+    if constexpr (CROSS) {
+        w.seq = u_.s;
+        w.kvh = u_.h;
+        w.j0 = u_.k * kBlockK;
+        if (!cross_lengths(p, w.seq, w.tok0, w.L, w.tokk0, w.Lk, w.Ls)) {
+            w.Ls = 0;
+            return false;
+        }
+        w.last = w.L == 0 || w.j0 + kBlockK >= w.Lk;
+        if (w.L == 0 || w.j0 >= w.Lk) return false;
+        w.jl = min(w.Lk, w.j0 + kBlockK) - 1;
+        w.t_lo = 0;
+        w.nt = (w.L + kBlockQ - 1) / kBlockQ;
+        w.ntiles = p.group * w.nt;
+        return true;
+    } else {
+    const int u = u_;
     const int per = p.num_seqs * p.Hkv;
     const int jb = u / per;           // causal: low key blocks are the heaviest
     const int r = u % per;
     w.seq = r / p.Hkv;
     w.kvh = r % p.Hkv;
-    w.j0 = jb * kBlockK;
-    w.tokk0 = w.Ls = 0;
     if (p.cu_seqlens) {
         w.tok0 = __ldg(p.cu_seqlens + w.seq);
         w.L = __ldg(p.cu_seqlens + w.seq + 1) - w.tok0;
@@ -144,28 +200,9 @@ __device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
         w.tok0 = w.seq * p.seqlen;
         w.L = p.seqlen;
     }
-    if constexpr (CROSS) {
-        if (p.cu_seqlens_k) {
-            w.tokk0 = __ldg(p.cu_seqlens_k + w.seq);
-            w.Lk = __ldg(p.cu_seqlens_k + w.seq + 1) - w.tokk0;
-            if (w.tokk0 < 0 || w.Lk < 0 || w.Lk > p.max_seqlen_k || w.tokk0 > p.total_k - w.Lk) {
-                report_error(kDevErrInput);
-                return false;
-            }
-            w.Ls = w.Lk;
-        } else {
-            w.tokk0 = w.seq * p.seqlen_k;
-            w.Lk = p.seq_lens_k ? __ldg(p.seq_lens_k + w.seq) : p.seqlen_k;
-            if (w.Lk < 0 || w.Lk > p.seqlen_k) {
-                report_error(kDevErrInput);
-                return false;
-            }
-            w.Ls = p.seqlen_k;
-        }
-    } else {
-        w.tokk0 = w.tok0;
-        w.Lk = w.L;
-    }
+    w.j0 = jb * kBlockK;
+    w.tokk0 = w.tok0;
+    w.Lk = w.L;
     if (w.L <= 0 || w.j0 >= w.Lk) return false;
     w.jl = min(w.Lk, w.j0 + kBlockK) - 1;
     const int nq = (w.L + kBlockQ - 1) / kBlockQ;
@@ -178,6 +215,7 @@ __device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
     w.nt = hi - lo;
     w.ntiles = p.group * w.nt;
     return w.nt > 0;
+    }
 }
 
 __device__ __forceinline__ void tile_of(const Unit &w, const Params &p, int k, int &h, int &q0) {
@@ -195,9 +233,35 @@ __device__ __forceinline__ int sched_unit(int it) {
     return (it & 1) ? (it + 1) * G - 1 - b : it * G + b;
 }
 
-#define FOR_EACH_UNIT(u)                                                  \
-    for (int it_ = 0, u = 0; it_ * (int)gridDim.x < p.num_units; ++it_)   \
-        if ((u = sched_unit(it_)) < p.num_units)
+struct UnitIndex {
+    int it, u;
+    __device__ __forceinline__ operator int() const { return u; }
+};
+// Cross attention: the units of this CTA's equal part (balance.cuh).
+template <bool CROSS, class S>
+__device__ __forceinline__ auto unit_walk(const S &sh) {
+    if constexpr (CROSS)
+        return BalanceWalk<CrossCost>(sh.balance);
+    else
+        return UnitIndex{0, 0};
+}
+template <bool CROSS, class S, class W>
+__device__ __forceinline__ bool unit_more(const Params &p, const S &sh, W &w) {
+    if constexpr (CROSS) {
+        return w.more(sh.balance);
+    } else {
+        for (; w.it * (int)gridDim.x < p.num_units; ++w.it)
+            if ((w.u = sched_unit(w.it)) < p.num_units) return true;
+        return false;
+    }
+}
+template <bool CROSS, class W>
+__device__ __forceinline__ void unit_step(const Params &p, W &w) {
+    if constexpr (CROSS) w.step(CrossCost{p}, p.num_seqs, p.Hkv);
+    else ++w.it;
+}
+#define FOR_EACH_BWD_UNIT(u)                                                                  \
+    for (auto u = unit_walk<CROSS>(sh); unit_more<CROSS>(p, sh, u); unit_step<CROSS>(p, u))
 
 struct Shared {
     uint64_t kv_full, kv_empty;
@@ -207,10 +271,13 @@ struct Shared {
     uint64_t ds_free[2];     // dK of the buffer's tile done: its dSᵀ buffer is free
     uint64_t acc_full, acc_free;
     uint64_t drain[2];
-    uint64_t kv_tail, qd_tail;   // cross attention: bytes of tiles with rows to clear
+    // cross attention: bytes of tiles with rows to clear; this CTA's part
+    uint64_t kv_tail, qd_tail;
+    Balance balance;
     uint32_t tmem_base;
     int abort;
 };
+static_assert(kSmemBytes + sizeof(Shared) <= 232448, "shared memory");
 
 // Cross attention: zeros over rows [valid, rows) of a tile of two 64-column
 // boxes, one warp.  What lies behind a sequence's end (other sequences,
@@ -231,7 +298,7 @@ __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const C
     const int lane = lane_id();
     float *rows = reinterpret_cast<float *>(smem + kOffRows);
     uint32_t uc = 0, n = 0, kv_tails = 0, qd_tails = 0;
-    FOR_EACH_UNIT(u) {
+    FOR_EACH_BWD_UNIT(u) {
         Unit w;
         if (!get_unit<CROSS>(u, p, w)) continue;
         if (!mbar_wait_warp(&sh.kv_empty, (uc & 1) ^ 1, abort)) goto out;
@@ -324,7 +391,7 @@ __device__ void mma_issuer_s(const Params &p, Shared &sh, uint8_t *smem) {
     const uint32_t vLo = desc_lo(smem_u32(smem + kOffV), 16);
     const uint32_t aStage = smem_u32(smem + kOffStage);
     uint32_t uc = 0, n = 0;
-    FOR_EACH_UNIT(u) {
+    FOR_EACH_BWD_UNIT(u) {
         Unit w;
         if (!get_unit<CROSS>(u, p, w)) continue;
         if (!mbar_wait(&sh.kv_full, uc & 1, abort)) goto out;
@@ -377,7 +444,7 @@ __device__ void mma_issuer_grad(const Params &p, Shared &sh, uint8_t *smem) {
     const uint32_t kLoMN = desc_lo(smem_u32(smem + kOffK), kKVBox);
     const uint32_t aStage = smem_u32(smem + kOffStage), aDS = smem_u32(smem + kOffDS);
     uint32_t uc = 0, m = 0;
-    FOR_EACH_UNIT(u) {
+    FOR_EACH_BWD_UNIT(u) {
         Unit w;
         if (!get_unit<CROSS>(u, p, w)) continue;
         if (!mbar_wait(&sh.kv_full, uc & 1, abort)) goto out;
@@ -503,17 +570,21 @@ __device__ void softmax_wg(const Params &p, Shared &sh, uint8_t *smem) {
     const float sl2 = p.scale_log2;
     uint32_t n = 0, uc = 0;
 
-    FOR_EACH_UNIT(u) {
+    FOR_EACH_BWD_UNIT(u) {
         Unit w;
         const bool any = get_unit<CROSS>(u, p, w);
         const int kj = w.j0 + r;                  // this thread's key
         uint16_t *dst = static_cast<uint16_t *>(wg ? p.dk : p.dv) +
                         ((size_t)(w.tokk0 + kj) * p.Hkv + w.kvh) * DH;
-        if (CROSS && kj < w.Ls && (!any || kj >= w.Lk)) {
-            // a key that no query sees
-            #pragma unroll
-            for (int c = 0; c < DH; c += 8)
-                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+        if (CROSS && w.last) {
+            // keys that no query sees
+            for (int i = (any ? w.Lk : 0) + r; i < w.Ls; i += kBlockK) {
+                uint16_t *row = static_cast<uint16_t *>(wg ? p.dk : p.dv) +
+                                ((size_t)(w.tokk0 + i) * p.Hkv + w.kvh) * DH;
+                #pragma unroll
+                for (int c = 0; c < DH; c += 8)
+                    *reinterpret_cast<uint4 *>(row + c) = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
         if (!any) continue;
         const bool key_ok = kj < w.Lk;
@@ -600,7 +671,7 @@ __device__ void dq_drain(const CUtensorMap *tmDQ, const Params &p, Shared &sh, u
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     float *stage = reinterpret_cast<float *>(smem + kOffDQ);
     uint32_t n = 0, hs = 0;
-    FOR_EACH_UNIT(u) {
+    FOR_EACH_BWD_UNIT(u) {
         Unit w;
         if (!get_unit<CROSS>(u, p, w)) continue;
         for (int k = 0; k < w.ntiles; ++k, ++n) {
@@ -684,6 +755,7 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         tma_prefetch_desc(&tmdO);
         tma_prefetch_desc(&tmDQ);
     }
+    if constexpr (CROSS) balance_begin<kThreads>(sh.balance, p.num_seqs, p.Hkv, CrossCost{p});
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

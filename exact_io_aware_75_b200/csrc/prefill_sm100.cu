@@ -34,6 +34,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "balance.cuh"
 #include "fa_internal.h"
 #include "sm100.cuh"
 
@@ -140,9 +141,60 @@ struct Unit {
     int ns[2], A;
 };
 
-template <bool PAGED, bool SINK = false, bool CROSS = false>
-__device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
+// Where a sequence's queries and keys lie; false if they do not fit.
+__device__ __forceinline__ bool cross_lengths(const Params &p, int s, int &tok0, int &L, int &tokk0,
+                                              int &Lk) {
+    if (p.cu_seqlens) {
+        tok0 = __ldg(p.cu_seqlens + s);
+        L = __ldg(p.cu_seqlens + s + 1) - tok0;
+        tokk0 = __ldg(p.cu_seqlens_k + s);
+        Lk = __ldg(p.cu_seqlens_k + s + 1) - tokk0;
+        return tok0 >= 0 && L >= 0 && L <= p.max_seqlen && tok0 <= p.total_tokens - L && tokk0 >= 0 &&
+               Lk >= 0 && Lk <= p.max_seqlen_k && tokk0 <= p.total_k - Lk;
+    }
+    tok0 = s * p.seqlen;
+    L = p.seqlen;
+    tokk0 = s * p.seqlen_k;
+    Lk = p.seq_lens_k ? __ldg(p.seq_lens_k + s) : p.seqlen_k;
+    return Lk >= 0 && Lk <= p.seqlen_k;
+}
+
+// What a sequence's units cost: a block of 128 keys for two row tiles 2.3 us,
+// for one 1.4, a unit's first loads and epilogue about as much as two blocks.
+struct CrossCost {
+    const Params &p;
+    __device__ __forceinline__ SeqCost operator()(int s, bool report) const {
+        int tok0, L, tokk0, Lk;
+        if (!cross_lengths(p, s, tok0, L, tokk0, Lk)) {
+            if (report && blockIdx.x == 0) report_error(kDevErrInput);
+            return SeqCost{0, 0, 0};
+        }
+        const int n = (L + 2 * kBlockM - 1) / (2 * kBlockM), nkb = (Lk + kBlockN - 1) / kBlockN;
+        const int unit = nkb * 5 + 8, rest = L - (n - 1) * 2 * kBlockM;
+        return SeqCost{n, unit, rest > kBlockM ? unit : nkb * 3 + 8};
+    }
+};
+
+template <bool PAGED, bool SINK = false, bool CROSS = false, class U>
+__device__ __forceinline__ bool get_unit(const U &u_, const Params &p, Unit &w) {
     int mb;
+    if constexpr (CROSS) {
+        w.seq = u_.s;
+        w.h = u_.h;
+        w.kvh = w.h / p.group;
+        mb = u_.k;
+        if (!cross_lengths(p, w.seq, w.tok0, w.L, w.tokk0, w.Lk)) return false;
+        w.q0 = mb * 2 * kBlockM;
+        if (w.q0 >= w.L) return false;
+        w.off = 0;
+        const int nkb = (w.Lk + kBlockN - 1) / kBlockN;
+        w.lo[0] = w.lo[1] = w.lo_all = 0;
+        w.hi[0] = w.hi_all = nkb;
+        w.hi[1] = w.q0 + kBlockM < w.L ? nkb : 0;
+        w.ns[0] = w.ns[1] = w.A = 0;
+        return true;
+    } else {
+    const int u = u_;
     if (PAGED) {
         // Chunked prefill: every row block of a chunk reads (nearly) the
         // sequence's whole cached context, which is far larger than the
@@ -193,27 +245,6 @@ __device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
         w.Lk = Lk;
         w.off = Lk - w.L;
     }
-    if constexpr (CROSS) {
-        int Lk = p.seqlen_k;
-        if (p.cu_seqlens_k) {
-            w.tokk0 = __ldg(p.cu_seqlens_k + w.seq);
-            Lk = __ldg(p.cu_seqlens_k + w.seq + 1) - w.tokk0;
-            if (w.tokk0 < 0 || Lk < 0 || Lk > p.max_seqlen_k || w.tokk0 > p.total_k - Lk) {
-                report_error(kDevErrInput);
-                return false;
-            }
-        } else {
-            w.tokk0 = w.seq * p.seqlen_k;
-            if (p.seq_lens_k) {
-                Lk = __ldg(p.seq_lens_k + w.seq);
-                if (Lk < 0 || Lk > p.seqlen_k) {
-                    report_error(kDevErrInput);
-                    return false;
-                }
-            }
-        }
-        w.Lk = Lk;
-    }
     const int nkb = (w.Lk + kBlockN - 1) / kBlockN;
     w.lo_all = 1 << 30;
     w.hi_all = 0;
@@ -239,6 +270,7 @@ __device__ __forceinline__ bool get_unit(int u, const Params &p, Unit &w) {
         w.A = min(max(w.ns[0], w.ns[1]), w.lo_all);
     }
     return true;
+    }
 }
 
 // The unit's key blocks in order: [0, A) (sink blocks), then [lo_all, hi_all).
@@ -259,12 +291,43 @@ __device__ __forceinline__ int sched_unit(int it) {
     for (int it_ = 0, u = 0; it_ * (int)gridDim.x < p.num_units; ++it_)   \
         if ((u = sched_unit(it_)) < p.num_units)
 
+// Cross attention: the units of this CTA's equal part (balance.cuh).
+struct UnitIndex {
+    int it, u;
+    __device__ __forceinline__ operator int() const { return u; }
+};
+template <bool CROSS, class S>
+__device__ __forceinline__ auto unit_walk(const S &sh) {
+    if constexpr (CROSS)
+        return BalanceWalk<CrossCost>(sh.balance);
+    else
+        return UnitIndex{0, 0};
+}
+template <bool CROSS, class S, class W>
+__device__ __forceinline__ bool unit_more(const Params &p, const S &sh, W &w) {
+    if constexpr (CROSS) {
+        return w.more(sh.balance);
+    } else {
+        for (; w.it * (int)gridDim.x < p.num_units; ++w.it)
+            if ((w.u = sched_unit(w.it)) < p.num_units) return true;
+        return false;
+    }
+}
+template <bool CROSS, class W>
+__device__ __forceinline__ void unit_step(const Params &p, W &w) {
+    if constexpr (CROSS) w.step(CrossCost{p}, p.num_seqs, p.Hq);
+    else ++w.it;
+}
+#define FOR_EACH_UNIT_OF(u, CROSS_)                                                       \
+    for (auto u = unit_walk<CROSS_>(sh); unit_more<CROSS_>(p, sh, u); unit_step<CROSS_>(p, u))
+
 struct Shared {
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full[2], p_lo[2], p_hi[2], o_full[2], o_empty[2];
     uint64_t drain;
     uint64_t v_tail;      // cross attention: bytes of a V tile with rows to clear
+    Balance balance; // and this CTA's part of the units
     uint32_t tmem_base;
     int abort;
 };
@@ -448,7 +511,7 @@ __device__ void producer_cross(const CUtensorMap *tmQ, const CUtensorMap *tmK,
     const int lane = lane_id();
     uint32_t q_uses[2] = {0, 0};
     uint32_t kv_it = 0, tails = 0;
-    FOR_EACH_UNIT(u) {
+    FOR_EACH_UNIT_OF(u, true) {
         Unit w;
         if (!get_unit<false, false, true>(u, p, w)) continue;
         for (int t = 0; t < 2; ++t) {
@@ -587,7 +650,7 @@ __device__ void mma_issuer(const Params &p, Shared &sh, uint8_t *sQ, uint8_t *sK
         return true;
     };
 
-    FOR_EACH_UNIT(u) {
+    FOR_EACH_UNIT_OF(u, CROSS) {
         Unit w;
         if (!get_unit<PAGED, SINK, CROSS>(u, p, w)) continue;
         bool first_pv[2] = {true, true};
@@ -727,7 +790,7 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
     const uint32_t tO = sh.tmem_base + lanes + C::kColO + t * D;
     uint32_t s_cnt = 0, pv_cnt = 0;
 
-    FOR_EACH_UNIT(u) {
+    FOR_EACH_UNIT_OF(u, CROSS) {
         Unit w;
         if (!get_unit<PAGED, SINK, CROSS>(u, p, w)) continue;
         // (selects, not w.lo[t]: a run-time index would keep the unit in
@@ -1017,6 +1080,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
+    if constexpr (CROSS) balance_begin<kThreads>(sh.balance, p.num_seqs, p.Hq, CrossCost{p});
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
