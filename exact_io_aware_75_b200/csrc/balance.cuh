@@ -1,115 +1,104 @@
-// balance.cuh -- equal shares of ragged work for a persistent grid.
+// balance.cuh -- ragged work dealt out evenly to a persistent grid.
 //
-// Sequences of different lengths give units of different cost: dealt out in
-// turn, the busiest of 148 CTAs with seven units each ends a third later than
-// the average (16 x 448 queries on 400 to 1,500 keys).  Here the units stand
-// in one row, sequence by sequence, head by head, and a CTA takes those that
-// begin in its part of the row's total cost.  No table and no limit on the
-// number of sequences: a scan over the sequences finds the one a part begins
-// in, and from there on the walk goes by the sequences' own lengths.
+// Sequences of different lengths give units of different cost; dealt out to
+// 148 CTAs as they come, the busiest ends well after the average.  Here the
+// sequences are ordered by the cost of their units first, dearest first, and
+// the units dealt in rows of gridDim.x, in alternating directions: units of a
+// row cost nearly the same, and CTAs at work at the same time share a sequence
+// and its keys.  (Equal contiguous parts of the units, the other way, were 11 %
+// slower on equal lengths.)  Each CTA orders the sequences for itself.  More
+// than kDealSeqs of them are dealt as they come: there are many units per CTA
+// then, and their costs average out.
 #pragma once
 
+#include <cstdint>
 #include <cuda_runtime.h>
 
 #include "sm100.cuh"
 
 namespace fa {
 
-// The units of one head of a sequence: n, all of cost `unit` but the last.
-struct SeqCost {
-    int n, unit, last;
-    __device__ __forceinline__ long long head() const {
-        return n > 0 ? (long long)(n - 1) * unit + last : 0;
+constexpr int kDealSeqs = 100;
+
+// The units of one head of a sequence: how many, and the cost of the first.
+struct SeqUnits {
+    int n, cost;
+};
+
+struct DealTable {
+    int first[kDealSeqs + 1];       // units before each sequence, in order
+    uint8_t order[kDealSeqs];
+};
+static_assert(sizeof(DealTable) <= 512, "the backward finds it 512 bytes");
+
+// All threads of a block of at least kDealSeqs; ends with a barrier.
+template <class F>
+__device__ __forceinline__ void deal_begin(DealTable &t, int num_seqs, int heads, F units) {
+    if (num_seqs > kDealSeqs) return;
+    const int s = threadIdx.x;
+    SeqUnits c{0, 0};
+    if (s < num_seqs) {
+        c = units(s);
+        t.first[s] = c.n > 0 ? c.cost : -1;
     }
-};
-
-// A unit: its sequence, head and place in the head.
-struct UnitAt {
-    int s, h, k;
-};
-
-struct Balance {
-    UnitAt first, end;     // this CTA's units: from `first` up to, not including, `end`
-    long long warp[16];
-};
-
-// All threads of the block; ends with a barrier.
-template <int THREADS, class F>
-__device__ __forceinline__ void balance_begin(Balance &b, int num_seqs, int heads, F cost) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long total = 0;
-    #pragma unroll 1
-    for (int s = tid; s < num_seqs; s += THREADS) total += cost(s, true).head();
-    #pragma unroll 1
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) b.warp[warp] = total;
-    if (tid == 0) b.first = b.end = UnitAt{num_seqs, 0, 0};
     __syncthreads();
-    total = 0;
-    #pragma unroll 1
-    for (int w = 0; w < THREADS / 32; ++w) total += b.warp[w];
-    total *= heads;
-    long long running = 0;
-    #pragma unroll 1
-    for (int s0 = 0; s0 < num_seqs; s0 += THREADS) {
-        const int s = s0 + tid;
-        const SeqCost c = s < num_seqs ? cost(s, false) : SeqCost{0, 0, 0};
-        long long inc = c.head();
+    int rank = 0;
+    if (s < num_seqs) {
+        const int mine = t.first[s];
         #pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+        for (int i = 0; i < num_seqs; ++i) {
+            const int x = t.first[i];
+            rank += x > mine || (x == mine && i < s);
         }
-        __syncthreads();
-        if (lane == 31) b.warp[warp] = inc;
-        __syncthreads();
-        long long before = running;
+    }
+    __syncthreads();
+    if (s < num_seqs) {
+        t.order[rank] = (uint8_t)s;
+        t.first[rank + 1] = c.n * heads;
+    }
+    if (s == 0) t.first[0] = 0;
+    __syncthreads();
+    if (s < 32) {
+        int running = 0;
         #pragma unroll 1
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) before += b.warp[w];
-            running += b.warp[w];
-        }
-        const long long head = c.head();
-        before = (before + inc - head) * heads;
-        // the bounds of this CTA's part that lie in this sequence
-        #pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-            const long long g = gridDim.x, i = blockIdx.x + e;
-            const long long off = total / g * i + total % g * i / g - before;
-            if (head == 0 || off < 0 || off >= head * heads) continue;
-            // the first unit that begins at or behind the bound
-            UnitAt u{s, (int)(off / head), 0};
-            u.k = (int)((off - u.h * head + c.unit - 1) / c.unit);
-            if (u.k >= c.n) {
-                u.k = 0;
-                if (++u.h == heads) {
-                    u.h = 0;
-                    do ++u.s;
-                    while (u.s < num_seqs && cost(u.s, false).n == 0);
-                }
+        for (int i0 = 1; i0 <= num_seqs; i0 += 32) {
+            const int i = i0 + s;
+            int x = i <= num_seqs ? t.first[i] : 0;
+            #pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (s >= o) x += y;
             }
-            if (e) b.end = u; else b.first = u;
+            if (i <= num_seqs) t.first[i] = running + x;
+            running += __shfl_sync(0xffffffffu, x, 31);
         }
     }
     __syncthreads();
 }
 
-// The units of this CTA's part, for each thread that walks them.  Three numbers
-// are kept; the rest is worked out again at each step, since the walkers'
-// inner loops have no registers to spare.
-template <class F>
-struct BalanceWalk : UnitAt {
-    __device__ __forceinline__ explicit BalanceWalk(const Balance &b) : UnitAt(b.first) {}
-    __device__ __forceinline__ bool more(const Balance &b) const {
-        return s != b.end.s || h != b.end.h || k != b.end.k;
-    }
-    __device__ __forceinline__ void step(F cost, int num_seqs, int heads) {
-        if (++k < cost(s, false).n) return;
-        k = 0;
-        if (++h < heads) return;
-        h = 0;
-        do ++s;
-        while (s < num_seqs && cost(s, false).n == 0);
+// The units of this CTA, for each thread that walks them: sequence, head and
+// place in the head.  Only `it` and `r` live across a unit.
+struct DealWalk {
+    int it = 0, r = 0, s, h, k;
+    __device__ __forceinline__ bool more(const DealTable &t, int num_seqs, int heads, int most) {
+        const int g = gridDim.x, i = blockIdx.x;
+        int u = (it & 1) ? (it + 1) * g - 1 - i : it * g + i;
+        if (num_seqs <= kDealSeqs) {
+            if (u >= t.first[num_seqs]) return false;     // (only the last row is short)
+            while (u >= t.first[r + 1]) ++r;
+            s = t.order[r];
+            u -= t.first[r];
+            k = u / heads;
+            h = u - k * heads;
+        } else {
+            const int per = num_seqs * heads;
+            k = u / per;
+            if (k >= most) return false;
+            u -= k * per;
+            s = u / heads;
+            h = u - s * heads;
+        }
+        return true;
     }
 };
 

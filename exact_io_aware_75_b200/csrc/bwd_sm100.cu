@@ -41,6 +41,7 @@
 //     allocation), warp 14 the three gradient GEMMs, so that a tile's S^T
 //     never waits behind the previous tile's gradients (which wait for that
 //     tile's softmax) and the two issue streams overlap.
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -143,22 +144,20 @@ __device__ __forceinline__ bool cross_lengths(const Params &p, int s, int &tok0,
     return Lk >= 0 && Lk <= p.seqlen_k;
 }
 
-// What a KV head's units of a sequence cost, in query tiles; a unit's K and V
-// and its dK and dV count as four.  The last unit also clears the gradients of
-// keys that no query sees; a sequence without any (query, key) pair has one
-// unit for that.
-struct CrossCost {
+// A sequence's units, by their query tiles.  The last unit also clears the
+// gradients of keys that no query sees; a sequence without any (query, key)
+// pair has one unit for that.
+struct CrossUnits {
     const Params &p;
-    __device__ __forceinline__ SeqCost operator()(int s, bool report) const {
+    __device__ __forceinline__ SeqUnits operator()(int s) const {
         int tok0, L, tokk0, Lk, Ls;
         if (!cross_lengths(p, s, tok0, L, tokk0, Lk, Ls)) {
-            if (report && blockIdx.x == 0) report_error(kDevErrInput);
-            return SeqCost{0, 0, 0};
+            report_error(kDevErrInput);
+            return SeqUnits{0, 0};
         }
-        if (Ls == 0) return SeqCost{0, 0, 0};
-        if (L == 0 || Lk == 0) return SeqCost{1, 1 + Ls / kBlockK, 1 + Ls / kBlockK};
-        const int unit = p.group * ((L + kBlockQ - 1) / kBlockQ) + 4;
-        return SeqCost{(Lk + kBlockK - 1) / kBlockK, unit, unit};
+        if (Ls == 0) return SeqUnits{0, 0};
+        if (L == 0 || Lk == 0) return SeqUnits{1, 0};
+        return SeqUnits{(Lk + kBlockK - 1) / kBlockK, (L + kBlockQ - 1) / kBlockQ};
     }
 };
 
@@ -169,12 +168,17 @@ __device__ __forceinline__ bool get_unit(const U &u_, const Params &p, Unit &w) 
         w.seq = u_.s;
         w.kvh = u_.h;
         w.j0 = u_.k * kBlockK;
+        w.last = false;
         if (!cross_lengths(p, w.seq, w.tok0, w.L, w.tokk0, w.Lk, w.Ls)) {
-            w.Ls = 0;
+            report_error(kDevErrInput);
             return false;
         }
-        w.last = w.L == 0 || w.j0 + kBlockK >= w.Lk;
-        if (w.L == 0 || w.j0 >= w.Lk) return false;
+        if (w.L == 0 || w.Lk == 0) {
+            w.last = u_.k == 0;
+            return false;
+        }
+        if (w.j0 >= w.Lk) return false;
+        w.last = w.j0 + kBlockK >= w.Lk;
         w.jl = min(w.Lk, w.j0 + kBlockK) - 1;
         w.t_lo = 0;
         w.nt = (w.L + kBlockQ - 1) / kBlockQ;
@@ -234,34 +238,22 @@ __device__ __forceinline__ int sched_unit(int it) {
 }
 
 struct UnitIndex {
-    int it, u;
+    int it = 0, u = 0;
     __device__ __forceinline__ operator int() const { return u; }
 };
-// Cross attention: the units of this CTA's equal part (balance.cuh).
-template <bool CROSS, class S>
-__device__ __forceinline__ auto unit_walk(const S &sh) {
-    if constexpr (CROSS)
-        return BalanceWalk<CrossCost>(sh.balance);
-    else
-        return UnitIndex{0, 0};
-}
+// (or cross attention's order of the units, balance.cuh)
 template <bool CROSS, class S, class W>
 __device__ __forceinline__ bool unit_more(const Params &p, const S &sh, W &w) {
     if constexpr (CROSS) {
-        return w.more(sh.balance);
+        return w.more(*sh.deal, p.num_seqs, p.Hkv, p.num_kblocks);
     } else {
         for (; w.it * (int)gridDim.x < p.num_units; ++w.it)
             if ((w.u = sched_unit(w.it)) < p.num_units) return true;
         return false;
     }
 }
-template <bool CROSS, class W>
-__device__ __forceinline__ void unit_step(const Params &p, W &w) {
-    if constexpr (CROSS) w.step(CrossCost{p}, p.num_seqs, p.Hkv);
-    else ++w.it;
-}
-#define FOR_EACH_BWD_UNIT(u)                                                                  \
-    for (auto u = unit_walk<CROSS>(sh); unit_more<CROSS>(p, sh, u); unit_step<CROSS>(p, u))
+#define FOR_EACH_BWD_UNIT(u)                                                               \
+    for (std::conditional_t<CROSS, DealWalk, UnitIndex> u; unit_more<CROSS>(p, sh, u); ++u.it)
 
 struct Shared {
     uint64_t kv_full, kv_empty;
@@ -271,9 +263,9 @@ struct Shared {
     uint64_t ds_free[2];     // dK of the buffer's tile done: its dSᵀ buffer is free
     uint64_t acc_full, acc_free;
     uint64_t drain[2];
-    // cross attention: bytes of tiles with rows to clear; this CTA's part
+    // cross attention: bytes of tiles with rows to clear; the order of the units
     uint64_t kv_tail, qd_tail;
-    Balance balance;
+    DealTable *deal;
     uint32_t tmem_base;
     int abort;
 };
@@ -755,7 +747,14 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         tma_prefetch_desc(&tmdO);
         tma_prefetch_desc(&tmDQ);
     }
-    if constexpr (CROSS) balance_begin<kThreads>(sh.balance, p.num_seqs, p.Hkv, CrossCost{p});
+    if constexpr (CROSS) {
+        // before the tiles or behind them: of the 1,024 bytes that align them
+        // one part holds 512
+        const int front = (int)(smem - smem_raw);
+        DealTable *deal = reinterpret_cast<DealTable *>(front >= 512 ? smem_raw : smem + kSmemBytes - 1024);
+        if (threadIdx.x == 0) sh.deal = deal;
+        deal_begin(*deal, p.num_seqs, p.Hkv, CrossUnits{p});
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -31,6 +31,7 @@
 //   * The epilogue divides O by l once ("FlashAttention-2": delayed
 //     normalisation) and writes O and LSE = ln2 * (m + log2 l).
 #include <climits>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -159,19 +160,16 @@ __device__ __forceinline__ bool cross_lengths(const Params &p, int s, int &tok0,
     return Lk >= 0 && Lk <= p.seqlen_k;
 }
 
-// What a sequence's units cost: a block of 128 keys for two row tiles 2.3 us,
-// for one 1.4, a unit's first loads and epilogue about as much as two blocks.
-struct CrossCost {
+// A sequence's units, by their key blocks.
+struct CrossUnits {
     const Params &p;
-    __device__ __forceinline__ SeqCost operator()(int s, bool report) const {
+    __device__ __forceinline__ SeqUnits operator()(int s) const {
         int tok0, L, tokk0, Lk;
         if (!cross_lengths(p, s, tok0, L, tokk0, Lk)) {
-            if (report && blockIdx.x == 0) report_error(kDevErrInput);
-            return SeqCost{0, 0, 0};
+            report_error(kDevErrInput);
+            return SeqUnits{0, 0};
         }
-        const int n = (L + 2 * kBlockM - 1) / (2 * kBlockM), nkb = (Lk + kBlockN - 1) / kBlockN;
-        const int unit = nkb * 5 + 8, rest = L - (n - 1) * 2 * kBlockM;
-        return SeqCost{n, unit, rest > kBlockM ? unit : nkb * 3 + 8};
+        return SeqUnits{(L + 2 * kBlockM - 1) / (2 * kBlockM), (Lk + kBlockN - 1) / kBlockN};
     }
 };
 
@@ -183,7 +181,10 @@ __device__ __forceinline__ bool get_unit(const U &u_, const Params &p, Unit &w) 
         w.h = u_.h;
         w.kvh = w.h / p.group;
         mb = u_.k;
-        if (!cross_lengths(p, w.seq, w.tok0, w.L, w.tokk0, w.Lk)) return false;
+        if (!cross_lengths(p, w.seq, w.tok0, w.L, w.tokk0, w.Lk)) {
+            report_error(kDevErrInput);
+            return false;
+        }
         w.q0 = mb * 2 * kBlockM;
         if (w.q0 >= w.L) return false;
         w.off = 0;
@@ -291,35 +292,23 @@ __device__ __forceinline__ int sched_unit(int it) {
     for (int it_ = 0, u = 0; it_ * (int)gridDim.x < p.num_units; ++it_)   \
         if ((u = sched_unit(it_)) < p.num_units)
 
-// Cross attention: the units of this CTA's equal part (balance.cuh).
+// The same, or cross attention's order of the units (balance.cuh).
 struct UnitIndex {
-    int it, u;
+    int it = 0, u = 0;
     __device__ __forceinline__ operator int() const { return u; }
 };
-template <bool CROSS, class S>
-__device__ __forceinline__ auto unit_walk(const S &sh) {
-    if constexpr (CROSS)
-        return BalanceWalk<CrossCost>(sh.balance);
-    else
-        return UnitIndex{0, 0};
-}
 template <bool CROSS, class S, class W>
 __device__ __forceinline__ bool unit_more(const Params &p, const S &sh, W &w) {
     if constexpr (CROSS) {
-        return w.more(sh.balance);
+        return w.more(sh.deal, p.num_seqs, p.Hq, p.num_mblocks);
     } else {
         for (; w.it * (int)gridDim.x < p.num_units; ++w.it)
             if ((w.u = sched_unit(w.it)) < p.num_units) return true;
         return false;
     }
 }
-template <bool CROSS, class W>
-__device__ __forceinline__ void unit_step(const Params &p, W &w) {
-    if constexpr (CROSS) w.step(CrossCost{p}, p.num_seqs, p.Hq);
-    else ++w.it;
-}
-#define FOR_EACH_UNIT_OF(u, CROSS_)                                                       \
-    for (auto u = unit_walk<CROSS_>(sh); unit_more<CROSS_>(p, sh, u); unit_step<CROSS_>(p, u))
+#define FOR_EACH_UNIT_OF(u, CROSS_)                                                        \
+    for (std::conditional_t<CROSS_, DealWalk, UnitIndex> u; unit_more<CROSS_>(p, sh, u); ++u.it)
 
 struct Shared {
     uint64_t q_full[2], q_empty[2];
@@ -327,7 +316,7 @@ struct Shared {
     uint64_t s_full[2], p_lo[2], p_hi[2], o_full[2], o_empty[2];
     uint64_t drain;
     uint64_t v_tail;      // cross attention: bytes of a V tile with rows to clear
-    Balance balance; // and this CTA's part of the units
+    DealTable deal;       // and the order of the units
     uint32_t tmem_base;
     int abort;
 };
@@ -1080,7 +1069,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    if constexpr (CROSS) balance_begin<kThreads>(sh.balance, p.num_seqs, p.Hq, CrossCost{p});
+    if constexpr (CROSS) deal_begin(sh.deal, p.num_seqs, p.Hq, CrossUnits{p});
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
