@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -197,8 +198,11 @@ def _check(rc: int, where: str):
         raise FAError(rc, where)
 
 
+_Tensor, _int32 = torch.Tensor, torch.int32
+
+
 def _need(t, dtype, ndim, name):
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda
             and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -476,14 +480,15 @@ def _out_pair(out, lse, o_shape, lse_shape, out_dtype, return_lse, like):
     if out is None:
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise FAError(FA_ERR_INVALID_ARG, f"out_dtype {out_dtype}")
-        out = like.new_empty(o_shape, dtype=out_dtype)
+        out = (torch.empty_like(like) if like.dtype is out_dtype and like.shape == o_shape
+               else like.new_empty(o_shape, dtype=out_dtype))
     else:
         _need(out, torch.float32 if out.dtype == torch.float32 else torch.bfloat16, len(o_shape), "out")
-        if tuple(out.shape) != tuple(o_shape):
+        if out.shape != o_shape:
             raise FAError(FA_ERR_INVALID_ARG, "out shape")
     if lse is not None:
         _need(lse, torch.float32, len(lse_shape), "lse")
-        if tuple(lse.shape) != tuple(lse_shape):
+        if lse.shape != lse_shape:
             raise FAError(FA_ERR_INVALID_ARG, "lse shape")
     elif return_lse:
         lse = like.new_empty(lse_shape, dtype=torch.float32)
@@ -509,6 +514,11 @@ def _like(t, ref, name):
     return torch.empty_like(ref) if t is None else _same(t, ref, name)
 
 
+@functools.lru_cache(maxsize=None)
+def _sm_count(device):
+    return torch.cuda.get_device_properties(device).multi_processor_count
+
+
 def _cross_shapes(q, k, v, ndim):
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, torch.bfloat16, ndim, n)
@@ -517,9 +527,11 @@ def _cross_shapes(q, k, v, ndim):
 
 
 def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, out=None, lse=None,
-              return_lse=True, stream=None):
+              return_lse=True, stream=None, split_keys=None):
     """Cross attention, dense.  q [B,Nq,Hq,d], k/v [B,Nk,Hkv,d] bf16, seq_lens_k [B] int32
-    (device) or None -> (O [B,Nq,Hq,d], LSE [B,Hq,Nq])."""
+    (device) or None -> (O [B,Nq,Hq,d], LSE [B,Hq,Nq]).  split_keys: through
+    decode_cross (bf16 O only), or not; by default where the queries are few, as include/fa.h
+    says there."""
     _cross_shapes(q, k, v, 4)
     B, Nq, Hq, d = q.shape
     Nk, Hkv = k.shape[1:3]
@@ -528,7 +540,14 @@ def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, ou
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     out, lse, od = _out_pair(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), out_dtype, return_lse, q)
-    with _device_of(q, k=k, v=v, seq_lens_k=seq_lens_k, out=out, lse=lse):
+    if split_keys is None:
+        # one SM per head and 256 queries fills a quarter of the GPU or less
+        # (32 of 148: 36 us against 40; 64: 60 against 58)
+        split_keys = (od == FA_OUT_BF16 and 0 < B * Hq * -(-Nq // 256) * 4 <= _sm_count(q.get_device())
+                      and Nk < 1 << 22 and decode_cross_workspace_bytes(B, Hq, max(Hkv, 1), Nq, d) > 0)
+    if split_keys:
+        return decode_cross(q, k, v, seq_lens_k, scale, out, lse, return_lse=False, stream=stream)
+    with _device_of(q, k, v, seq_lens_k, out, lse):
         _check(_lib.fa_fwd_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(seq_lens_k),
                                  B, Hq, Hkv, Nq, Nk, d, float(scale), od, _stream(stream)),
                "fa_fwd_cross")
@@ -547,8 +566,8 @@ def fwd_varlen_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     out, lse, od = _out_pair(out, lse, (Tq, Hq, d), (Hq, Tq), out_dtype, return_lse, q)
-    with _device_of(q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out,
-                    lse=lse):
+    with _device_of(q, k, v, cu_seqlens_q, cu_seqlens_k, out,
+                    lse):
         _check(_lib.fa_fwd_varlen_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
                                         _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
                                         cu_seqlens_q.numel() - 1, Tq, Tk, int(max_seqlen_q),
@@ -575,8 +594,8 @@ def bwd_cross(q, k, v, o, dout, lse, seq_lens_k=None, scale=None, dq=None, dk=No
         scale = 1.0 / math.sqrt(d)
     dq, dk, dv = _like(dq, q, "dq"), _like(dk, k, "dk"), _like(dv, v, "dv")
     workspace = _bytes_of(workspace, bwd_workspace_bytes(B * Nq, Hq, d), q)
-    with _device_of(q, k=k, v=v, o=o, dout=dout, lse=lse, seq_lens_k=seq_lens_k, dq=dq, dk=dk,
-                    dv=dv, workspace=workspace):
+    with _device_of(q, k, v, o, dout, lse, seq_lens_k, dq, dk,
+                    dv, workspace):
         _check(_lib.fa_bwd_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
                                  _ptr(dq), _ptr(dk), _ptr(dv), _ptr(seq_lens_k), B, Hq, Hkv, Nq,
                                  Nk, d, float(scale), _ptr(workspace),
@@ -603,8 +622,8 @@ def bwd_varlen_cross(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seql
         scale = 1.0 / math.sqrt(d)
     dq, dk, dv = _like(dq, q, "dq"), _like(dk, k, "dk"), _like(dv, v, "dv")
     workspace = _bytes_of(workspace, bwd_workspace_bytes(Tq, Hq, d), q)
-    with _device_of(q, k=k, v=v, o=o, dout=dout, lse=lse, cu_seqlens_q=cu_seqlens_q,
-                    cu_seqlens_k=cu_seqlens_k, dq=dq, dk=dk, dv=dv, workspace=workspace):
+    with _device_of(q, k, v, o, dout, lse, cu_seqlens_q,
+                    cu_seqlens_k, dq, dk, dv, workspace):
         _check(_lib.fa_bwd_varlen_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
                                         _ptr(dq), _ptr(dk), _ptr(dv), _ptr(cu_seqlens_q),
                                         _ptr(cu_seqlens_k), cu_seqlens_q.numel() - 1, Tq, Tk,
@@ -646,9 +665,9 @@ def decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_
         scale = 1.0 / math.sqrt(d)
     out, lse = _decode_out(out, lse, (S, Hq, d), (S, Hq), return_lse, q)
     workspace = _bytes_of(workspace, decode_shared_workspace_bytes(S, Hq, max(Hkv, 1), d), q)
-    with _device_of(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                    seq_lens=seq_lens, cu_groups=cu_groups, prefix_lens=prefix_lens, sinks=sinks,
-                    out=out, lse=lse, workspace=workspace):
+    with _device_of(q, k_cache, v_cache, block_table,
+                    seq_lens, cu_groups, prefix_lens, sinks,
+                    out, lse, workspace):
         _check(_lib.fa_decode_shared(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
                                      _ptr(seq_lens), _ptr(cu_groups), _ptr(prefix_lens),
                                      _ptr(out), _ptr(lse), _ptr(sinks), S, groups, P, Hq, Hkv, d,
@@ -676,7 +695,7 @@ def decode_cross(q, k, v, seq_lens_k=None, scale=None, out=None, lse=None, retur
         scale = 1.0 / math.sqrt(d)
     out, lse = _decode_out(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), return_lse, q)
     workspace = _bytes_of(workspace, decode_cross_workspace_bytes(B, Hq, max(Hkv, 1), Nq, d), q)
-    with _device_of(q, k=k, v=v, seq_lens_k=seq_lens_k, out=out, lse=lse, workspace=workspace):
+    with _device_of(q, k, v, seq_lens_k, out, lse, workspace):
         _check(_lib.fa_decode_cross(_ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens_k), _ptr(out),
                                     _ptr(lse), B, Hq, Hkv, Nq, Nk, d, float(scale),
                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -794,12 +813,12 @@ def decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, scale=None,
 _same_device = contextlib.nullcontext()
 
 
-def _device_of(first, **others):
+def _device_of(first, *others):
     """A context in which the device of `first` is current; the others must be on it."""
     device = first.get_device()
-    for name, t in others.items():
+    for t in others:
         if t is not None and t.get_device() != device:
-            raise FAError(FA_ERR_INVALID_ARG, f"{name} is on {t.device}, not {first.device}")
+            raise FAError(FA_ERR_INVALID_ARG, f"a tensor on {t.device}, others on {first.device}")
     return _same_device if device == torch.cuda.current_device() else torch.cuda.device(device)
 
 
@@ -827,7 +846,10 @@ def _need_cache(k_cache, v_cache, k_scale, v_scale):
 
 
 def _need_ints(shape, name, t):
-    _need(t, torch.int32, len(shape), name)
+    if (isinstance(t, _Tensor) and t.dtype is _int32 and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
+        return
+    _need(t, _int32, len(shape), name)
     if t.shape != shape:
         raise FAError(FA_ERR_INVALID_ARG, f"{name} shape {tuple(t.shape)}, not {tuple(shape)}")
 
@@ -860,10 +882,10 @@ def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, fre
     _need_ints((N, maxp), "block_table_out", block_table_out)
     _need_ints((N,), "seq_lens_out", seq_lens_out)
     _need_ints((1,), "free_count_out", free_count_out)
-    with _device_of(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                    block_table=block_table, seq_lens=seq_lens, parents=parents,
-                    free_pages=free_pages, free_count=free_count, block_table_out=block_table_out,
-                    seq_lens_out=seq_lens_out, free_count_out=free_count_out):
+    with _device_of(k_cache, v_cache, k_scale, v_scale,
+                    block_table, seq_lens, parents,
+                    free_pages, free_count, block_table_out,
+                    seq_lens_out, free_count_out):
         _check(_lib.fa_cache_fork(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), eb,
                                   _ptr(block_table), _ptr(seq_lens), S, _ptr(parents), N,
                                   _ptr(free_pages), _ptr(free_count), free_pages.shape[0],
@@ -894,10 +916,10 @@ def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, 
     _need_ints((1,), "free_count", free_count)
     _need_ints((S,), "seq_lens_out", seq_lens_out)
     _need_ints((1,), "free_count_out", free_count_out)
-    with _device_of(k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new, cu_new=cu_new,
-                    block_table=block_table, seq_lens=seq_lens, free_pages=free_pages,
-                    free_count=free_count, seq_lens_out=seq_lens_out,
-                    free_count_out=free_count_out):
+    with _device_of(k_cache, v_cache, k_new, v_new, cu_new,
+                    block_table, seq_lens, free_pages,
+                    free_count, seq_lens_out,
+                    free_count_out):
         _check(_lib.fa_cache_append(_ptr(k_new), _ptr(v_new), _ptr(cu_new), S, T, _ptr(k_cache),
                                     _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
                                     _ptr(free_pages), _ptr(free_count), free_pages.shape[0],
@@ -911,7 +933,7 @@ def cache_copy_pages(k_cache, v_cache, src, dst, k_scale=None, v_scale=None, str
     P, ps, Hkv, d = k_cache.shape
     _need(src, torch.int32, 1, "src")
     _need_ints(src.shape, "dst", dst)
-    with _device_of(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, src=src, dst=dst):
+    with _device_of(k_cache, v_cache, k_scale, v_scale, src, dst):
         _check(_lib.fa_cache_copy_pages(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                         eb, _ptr(src), _ptr(dst), src.shape[0], P, Hkv, d, ps,
                                         _stream(stream)), "fa_cache_copy_pages")
@@ -932,8 +954,8 @@ def cache_collect(block_table, seq_lens, free_pages, free_count, page_size=16, w
     _need_ints((S,), "seq_lens", seq_lens)
     _need_ints((1,), "free_count", free_count)
     workspace = _bytes_of(workspace, cache_collect_workspace_bytes(P), block_table)
-    with _device_of(block_table, seq_lens=seq_lens, free_pages=free_pages, free_count=free_count,
-                    workspace=workspace):
+    with _device_of(block_table, seq_lens, free_pages, free_count,
+                    workspace):
         _check(_lib.fa_cache_collect(_ptr(block_table), _ptr(seq_lens), S, maxp, P,
                                      int(page_size), _ptr(free_pages), _ptr(free_count),
                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -958,9 +980,9 @@ def cache_compact(k_cache, v_cache, block_table, seq_lens, block_table_out, free
     _need_ints((P,), "free_pages", free_pages)
     _need_ints((1,), "free_count", free_count)
     workspace = _bytes_of(workspace, cache_compact_workspace_bytes(P), k_cache)
-    with _device_of(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                    block_table=block_table, seq_lens=seq_lens, block_table_out=block_table_out,
-                    free_pages=free_pages, free_count=free_count, workspace=workspace):
+    with _device_of(k_cache, v_cache, k_scale, v_scale,
+                    block_table, seq_lens, block_table_out,
+                    free_pages, free_count, workspace):
         _check(_lib.fa_cache_compact(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                      eb, _ptr(block_table), _ptr(seq_lens), S,
                                      _ptr(block_table_out), _ptr(free_pages), _ptr(free_count), P,

@@ -148,13 +148,14 @@ __device__ __forceinline__ int few_q(int b) { return b * 12288; }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// A sequence's length, clamped to what its table (or its stored keys) can hold.
+// A sequence's length.  One that its table cannot hold is clamped; one that its
+// stored keys cannot hold counts as none, and the combine leaves its rows alone.
 template <bool PAGED>
 __device__ __forceinline__ int good_length(const Params &p, int L) {
     const int most = PAGED ? p.max_pages * kPage : p.Nk;
     if (L < 0 || L > most) {
         if (blockIdx.x == 0) report_error(kDevErrInput);
-        L = L < 0 ? 0 : most;
+        L = L < 0 || !PAGED ? 0 : most;
     }
     return L;
 }
@@ -1306,6 +1307,8 @@ shared_combine_kernel(const Params p, uint16_t *__restrict__ o, float *__restric
             take(1, s.y + row / kRows, row % kRows);
         }
     } else {
+        const int len = p.lens ? __ldg(p.lens + tok / p.Nq) : 0;
+        if (len < 0 || len > p.Nk) return;
         const int row = (tok % p.Nq) * p.G + h % p.G;
         take(0, tok / p.Nq * p.pairs + row / kRows, row % kRows);
     }

@@ -374,12 +374,12 @@ int fa_decode_shared(const void *q, const void *k_cache, const void *v_cache,
 /*
  * Cross attention of few queries: the decoder's next token (Nq = 1), or the
  * few of a speculated step, against its encoder states.  fa_fwd_cross's
- * layouts, result and treatment of rows behind seq_lens_k (which may be NULL),
- * with o bf16; the keys are split over the whole GPU ("Flash-Decoding"),
- * where fa_fwd_cross gives each 256 queries of a head to one SM: the better
- * call while B * Hq * ceil(Nq / 256) is below the number of SMs or Nq * Hq /
- * Hkv is small.  A length outside [0, Nk] is clamped and reported
- * (fa_check_device_error, FA_ERR_INVALID_ARG).
+ * layouts, result, treatment of rows behind seq_lens_k (which may be NULL) and
+ * of lengths that do not fit, with o bf16.  The keys are split over the whole
+ * GPU ("Flash-Decoding"), where fa_fwd_cross gives each 256 queries of a head
+ * to one SM: the faster call while those are fewer than a quarter of the SMs
+ * (B * Hq * ceil(Nq / 256); 30 queries, 16 heads, 4,000 keys 19 us against 62)
+ * or Nq * Hq / Hkv is small.
  *   workspace   fa_decode_cross_workspace_bytes(...) bytes, 256-byte aligned,
  *               not to be shared by calls that may overlap on the GPU.
  *   Hq / Hkv at most 128, Nq * Hq / Hkv at most 524288 (else

@@ -34,7 +34,7 @@ def poison(x, keep):
     return x
 
 
-def dense(fa, B, Hq, Hkv, Nq, Nk, d, lens=None, out_dtype=torch.bfloat16, seed=0, scale=None):
+def dense(fa, B, Hq, Hkv, Nq, Nk, d, lens=None, out_dtype=torch.bfloat16, seed=0, scale=None, split=False):
     """One forward and backward; rows behind the visible keys hold NaN."""
     g = torch.Generator().manual_seed(seed)
     q, do = rand((B, Nq, Hq, d), g), rand((B, Nq, Hq, d), g)
@@ -43,7 +43,7 @@ def dense(fa, B, Hq, Hkv, Nq, Nk, d, lens=None, out_dtype=torch.bfloat16, seed=0
     for b, n in enumerate(lens or []):
         k[b, n:], v[b, n:] = math.nan, math.nan
     Q, K, V, DO, L = q.cuda(), k.cuda(), v.cuda(), do.cuda(), i32(lens)
-    o, lse = fa.fwd_cross(Q, K, V, L, scale, out_dtype=out_dtype)
+    o, lse = fa.fwd_cross(Q, K, V, L, scale, out_dtype=out_dtype, split_keys=split)
     ob = o if o.dtype == torch.bfloat16 else fa.fwd_cross(Q, K, V, L, scale)[0]
     dk, dv = torch.full_like(K, math.nan), torch.full_like(V, math.nan)
     dq, dk, dv = fa.bwd_cross(Q, K, V, ob, DO, lse, L, scale, dk=dk, dv=dv)
@@ -72,8 +72,15 @@ def dense(fa, B, Hq, Hkv, Nq, Nk, d, lens=None, out_dtype=torch.bfloat16, seed=0
     (4, 2, 2, 40, 130, 128, [2, 128, 64, 130]),
     (2, 2, 1, 3, 5, 64, [0, 0]),
 ])
-def test_dense(fa, B, Hq, Hkv, Nq, Nk, d, lens):
-    dense(fa, B, Hq, Hkv, Nq, Nk, d, lens, seed=Nq + Nk)
+@pytest.mark.parametrize("split", [False, True, None])
+def test_dense(fa, B, Hq, Hkv, Nq, Nk, d, lens, split):
+    dense(fa, B, Hq, Hkv, Nq, Nk, d, lens, seed=Nq + Nk, split=split)
+
+
+def test_many_sequences(fa):
+    """More sequences than are ordered by cost; empty ones among them."""
+    dense(fa, 130, 2, 1, 20, 150, 64, [(37 * i) % 151 for i in range(130)], seed=2)
+    packed(fa, [(11 * i) % 40 for i in range(140)], [(29 * i) % 170 for i in range(140)], 2, 2, 128, seed=3)
 
 
 def test_fp32_output_and_scale(fa):
@@ -128,7 +135,8 @@ def test_packed(fa, nq, nk, Hq, Hkv, d, gap):
     packed(fa, nq, nk, Hq, Hkv, d, sum(nq) + sum(nk), gap)
 
 
-def test_large_scores(fa):
+@pytest.mark.parametrize("split", [False, True])
+def test_large_scores(fa, split):
     """Scores of several hundred: one key takes nearly all the weight, and the conditional rescale runs often.  The
     scores' fp32 sums err by 2^-24 d sum |q k| scale there; inputs whose products are whole numbers make them exact."""
     g = torch.Generator().manual_seed(11)
@@ -136,7 +144,7 @@ def test_large_scores(fa):
     q = torch.randint(-3, 4, (B, Nq, H, d), generator=g).to(torch.bfloat16)
     k = torch.randint(-3, 4, (B, Nk, H, d), generator=g).to(torch.bfloat16)
     v = rand((B, Nk, H, d), g)
-    o, lse = fa.fwd_cross(q.cuda(), k.cuda(), v.cuda(), scale=1.0)
+    o, lse = fa.fwd_cross(q.cuda(), k.cuda(), v.cuda(), scale=1.0, split_keys=split)
     assert fa.check_device_error() == 0
     want = attend(q[0], k[0], v[0], 1.0)
     check(o[0], want["o"], "O")
@@ -149,9 +157,9 @@ def test_bad_lengths(fa):
     """Offsets or lengths that do not fit: the sequence is skipped and reported, the others are computed."""
     g = torch.Generator().manual_seed(3)
     q, k, v = rand((3, 20, 2, 64), g), rand((3, 40, 2, 64), g), rand((3, 40, 2, 64), g)
-    for bad in (-1, 41):
+    for bad, split in ((-1, False), (41, False), (-1, True), (41, True)):
         o = torch.full((3, 20, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
-        _, lse = fa.fwd_cross(q.cuda(), k.cuda(), v.cuda(), i32([40, bad, 17]), out=o)
+        _, lse = fa.fwd_cross(q.cuda(), k.cuda(), v.cuda(), i32([40, bad, 17]), out=o, split_keys=split)
         assert fa.check_device_error() == fa.FA_ERR_INVALID_ARG
         assert (o[1] == 5.0).all()
         check(o[2], attend(q[2], k[2, :17], v[2, :17], 0.125)["o"], "O")
@@ -175,9 +183,9 @@ def test_grouped_heads_equal_repeated(fa):
     g = torch.Generator().manual_seed(5)
     q, do = rand((2, 90, 6, 128), g).cuda(), rand((2, 90, 6, 128), g).cuda()
     k, v = rand((2, 200, 2, 128), g).cuda(), rand((2, 200, 2, 128), g).cuda()
-    o, lse = fa.fwd_cross(q, k, v)
+    o, lse = fa.fwd_cross(q, k, v, split_keys=False)
     kr, vr = k.repeat_interleave(3, 2).contiguous(), v.repeat_interleave(3, 2).contiguous()
-    o2, lse2 = fa.fwd_cross(q, kr, vr)
+    o2, lse2 = fa.fwd_cross(q, kr, vr, split_keys=False)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     _, dk, dv = fa.bwd_cross(q, k, v, o, do, lse)
     _, dk2, dv2 = fa.bwd_cross(q, kr, vr, o2, do, lse2)

@@ -348,7 +348,7 @@ def test_cross_is_fwd_cross(fa):
     k, v = (torch.randn((3, 1500, 2, 128), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
     lens = i32([1500, 3, 800])
     o, lse = fa.decode_cross(q, k, v, lens)
-    o2, lse2 = fa.fwd_cross(q, k, v, lens)
+    o2, lse2 = fa.fwd_cross(q, k, v, lens, split_keys=False)
     assert fa.check_device_error() == 0
     # both round P and O to bf16 their own way: |v| < 6, weights sum to one
     assert (o.float() - o2.float()).abs().max() <= 4 * 2.0 ** -8 * 6
@@ -356,8 +356,10 @@ def test_cross_is_fwd_cross(fa):
 
 
 def test_cross_bad_length(fa):
-    t = torch.ones((2, 1, 2, 64), dtype=torch.bfloat16, device="cuda")
-    k = torch.ones((2, 40, 2, 64), dtype=torch.bfloat16, device="cuda")
-    o, lse = fa.decode_cross(t, k, k, i32([-1, 50]))
+    """As fa_fwd_cross: the sequence is skipped, its rows left as they were, and reported."""
+    t = torch.ones((3, 1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    k = torch.ones((3, 40, 2, 64), dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.full_like(t, 5.0), torch.full((3, 2, 1), 5.0, device="cuda")
+    fa.decode_cross(t, k, k, i32([-1, 41, 40]), out=o, lse=lse)
     assert fa.check_device_error() == fa.FA_ERR_INVALID_ARG
-    assert (o[0] == 0).all() and torch.isneginf(lse[0]).all() and (o[1] == 1).all()
+    assert (o[:2] == 5).all() and (lse[:2] == 5).all() and (o[2] == 1).all()
