@@ -534,6 +534,7 @@ __device__ void producer(const CUtensorMap *tm, const Params &p, const Table &ta
             tma_load_3d(dst + lane * C::kBoxBytes, tm, bar, lane * 64, kvh,
                         w.it.src * p.Nk + j * kBlockN);
         }
+        __syncwarp();
         if (V && pending >= 0 && !clear()) {
             it += 2;
             goto out;
