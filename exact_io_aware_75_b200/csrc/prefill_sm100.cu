@@ -124,6 +124,11 @@ struct Params {
     // visible; packed: cu_seqlens_k.
     const int *cu_seqlens_k;
     int seqlen_k, total_k, max_seqlen_k;
+    // A row tile of cross attention holds `pack` query heads of one KV head
+    // (its group, if that fits) of each of tile_tok tokens: without an order
+    // between queries and keys they are rows like others, and 30 tokens of 4
+    // heads fill one tile instead of a quarter of four.
+    int pack, tile_tok;
 };
 
 struct Unit {
@@ -169,7 +174,7 @@ struct CrossUnits {
             report_error(kDevErrInput);
             return SeqUnits{0, 0};
         }
-        return SeqUnits{(L + 2 * kBlockM - 1) / (2 * kBlockM), (Lk + kBlockN - 1) / kBlockN};
+        return SeqUnits{(L + 2 * p.tile_tok - 1) / (2 * p.tile_tok), (Lk + kBlockN - 1) / kBlockN};
     }
 };
 
@@ -178,20 +183,20 @@ __device__ __forceinline__ bool get_unit(const U &u_, const Params &p, Unit &w) 
     int mb;
     if constexpr (CROSS) {
         w.seq = u_.s;
-        w.h = u_.h;
+        w.h = u_.h * p.pack;
         w.kvh = w.h / p.group;
         mb = u_.k;
         if (!cross_lengths(p, w.seq, w.tok0, w.L, w.tokk0, w.Lk)) {
             report_error(kDevErrInput);
             return false;
         }
-        w.q0 = mb * 2 * kBlockM;
+        w.q0 = mb * 2 * p.tile_tok;
         if (w.q0 >= w.L) return false;
         w.off = 0;
         const int nkb = (w.Lk + kBlockN - 1) / kBlockN;
         w.lo[0] = w.lo[1] = w.lo_all = 0;
         w.hi[0] = w.hi_all = nkb;
-        w.hi[1] = w.q0 + kBlockM < w.L ? nkb : 0;
+        w.hi[1] = w.q0 + p.tile_tok < w.L ? nkb : 0;
         w.ns[0] = w.ns[1] = w.A = 0;
         return true;
     } else {
@@ -300,7 +305,7 @@ struct UnitIndex {
 template <bool CROSS, class S, class W>
 __device__ __forceinline__ bool unit_more(const Params &p, const S &sh, W &w) {
     if constexpr (CROSS) {
-        return w.more(sh.deal, p.num_seqs, p.Hq, p.num_mblocks);
+        return w.more(sh.deal, p.num_seqs, p.Hq / p.pack, p.num_mblocks);
     } else {
         for (; w.it * (int)gridDim.x < p.num_units; ++w.it)
             if ((w.u = sched_unit(w.it)) < p.num_units) return true;
@@ -507,10 +512,10 @@ __device__ void producer_cross(const CUtensorMap *tmQ, const CUtensorMap *tmK,
             if (w.lo[t] >= w.hi[t]) continue;
             if (!mbar_wait_warp(&sh.q_empty[t], (q_uses[t] & 1) ^ 1, abort)) goto out;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&sh.q_full[t], C::kTileBytes);
+                mbar_arrive_expect_tx(&sh.q_full[t], p.tile_tok * p.pack * D * 2);
                 for (int b = 0; b < C::kBoxes; ++b)
                     tma_load_3d(sQ + t * C::kTileBytes + b * C::kBoxBytes, tmQ, &sh.q_full[t],
-                                b * C::kBoxCols, w.h, w.tok0 + w.q0 + t * kBlockM);
+                                b * C::kBoxCols, w.h, w.tok0 + w.q0 + t * p.tile_tok);
             }
             ++q_uses[t];
         }
@@ -777,6 +782,7 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = sh.tmem_base + lanes + t * kBlockN;
     const uint32_t tO = sh.tmem_base + lanes + C::kColO + t * D;
+    const int r_tok = CROSS ? r / p.pack : 0, r_head = CROSS ? r % p.pack : 0;
     uint32_t s_cnt = 0, pv_cnt = 0;
 
     FOR_EACH_UNIT_OF(u, CROSS) {
@@ -786,16 +792,19 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
         // local memory)
         const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
         const int ns = SINK ? (t ? w.ns[1] : w.ns[0]) : 0;   // sink blocks before lo
-        const int row = w.q0 + t * kBlockM + r;    // row index within the sequence
+        // the row's token, and (cross attention) its head
+        const int row = CROSS ? w.q0 + t * p.tile_tok + r_tok : w.q0 + t * kBlockM + r;
+        const int head = CROSS ? w.h + r_head : w.h;
+        const bool valid = row < w.L && (!CROSS || r_tok < p.tile_tok);
         if (lo >= hi) {
-            if (CROSS && row < w.L) {              // no key at all: O = 0, LSE = -inf
-                const size_t at = ((size_t)(w.tok0 + row) * p.Hq + w.h) * D;
+            if (CROSS && valid && w.lo_all >= w.hi_all) {     // no key at all: O = 0, LSE = -inf
+                const size_t at = ((size_t)(w.tok0 + row) * p.Hq + head) * D;
                 char *dst = static_cast<char *>(p.o) + at * (p.o_fp32 ? 4 : 2);
                 for (int c = 0; c < D * (p.o_fp32 ? 4 : 2); c += 16)
                     *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
                 if (p.lse)
-                    p.lse[p.cu_seqlens ? (size_t)w.h * p.total_tokens + w.tok0 + row
-                                       : ((size_t)w.seq * p.Hq + w.h) * p.seqlen + row] = -INFINITY;
+                    p.lse[p.cu_seqlens ? (size_t)head * p.total_tokens + w.tok0 + row
+                                       : ((size_t)w.seq * p.Hq + head) * p.seqlen + row] = -INFINITY;
             }
             continue;
         }
@@ -970,7 +979,6 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
         float inv_scale_o = 1.f;
         if (!mbar_wait_warp(&sh.o_full[t], (pv_cnt - 1) & 1, abort)) return;
         tc_fence_after();
-        const bool valid = row < w.L;
         if (p.sinks) {
             // Learned sink: one more denominator term 2^(z*log2e - m) of a
             // key whose value is zero; the reference max takes it in too.
@@ -984,7 +992,7 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
             }
         }
         const float inv_l = (l > 0.f) ? inv_scale_o * sv / l : 0.f;
-        const size_t orow = ((size_t)(w.tok0 + row) * p.Hq + w.h) * D;
+        const size_t orow = ((size_t)(w.tok0 + row) * p.Hq + head) * D;
         #pragma unroll
         for (int c = 0; c < D; c += 32) {
             uint32_t ov[32];
@@ -1020,9 +1028,9 @@ __device__ void softmax_wg(const Params &p, Shared &sh, int *kdoc) {
             const float lse2 = (l > 0.f) ? m_ref + __log2f(l) : -INFINITY;
             size_t idx;
             if (p.cu_seqlens)
-                idx = (size_t)w.h * p.total_tokens + w.tok0 + row;
+                idx = (size_t)head * p.total_tokens + w.tok0 + row;
             else
-                idx = ((size_t)w.seq * p.Hq + w.h) * p.seqlen + row;
+                idx = ((size_t)w.seq * p.Hq + head) * p.seqlen + row;
             p.lse[idx] = lse2 * 0.69314718055994531f;
         }
     }
@@ -1069,7 +1077,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    if constexpr (CROSS) deal_begin(sh.deal, p.num_seqs, p.Hq, CrossUnits{p});
+    if constexpr (CROSS) deal_begin(sh.deal, p.num_seqs, p.Hq / p.pack, CrossUnits{p});
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1154,6 +1162,9 @@ Params make_params(const PrefillArgs &a) {
     p.seqlen_k = a.seqlen_k;
     p.total_k = a.total_k;
     p.max_seqlen_k = a.max_seqlen_k;
+    p.pack = p.group <= kBlockM ? p.group : 1;
+    p.tile_tok = kBlockM / p.pack;
+    if (a.cross) p.num_mblocks = (a.max_seqlen + 2 * p.tile_tok - 1) / (2 * p.tile_tok);
     return p;
 }
 
@@ -1169,15 +1180,16 @@ int launch_d(const PrefillArgs &a, cudaStream_t stream) {
     const bool no_keys = a.cross && a.total_k == 0;
     const void *k = no_keys ? a.q : a.k, *v = no_keys ? a.q : a.v;
     const uint32_t kv_box = a.paged ? kPageRows : kBlockN;
+    Params p = make_params(a);
+    const uint32_t q_heads = a.cross ? p.pack : 1, q_toks = a.cross ? p.tile_tok : kBlockM;
     if (encode_tensor_map_3d(&tq, a.q, 2, D, a.Hq, T, (uint64_t)D * 2, (uint64_t)a.Hq * D * 2,
-                             64, 1, kBlockM, 128) ||
+                             64, q_heads, q_toks, 128) ||
         encode_tensor_map_3d(&tk, k, 2, D, a.Hkv, TK, (uint64_t)D * 2, (uint64_t)a.Hkv * D * 2,
                              64, 1, kv_box, 128) ||
         encode_tensor_map_3d(&tv, v, 2, D, a.Hkv, TK, (uint64_t)D * 2, (uint64_t)a.Hkv * D * 2,
                              64, 1, kv_box, 128))
         return -5;
-    Params p = make_params(a);
-    const long long units = (long long)p.num_mblocks * a.num_seqs * a.Hq;
+    const long long units = (long long)p.num_mblocks * a.num_seqs * (a.Hq / q_heads);
     if (units <= 0) return 0;
     if (units > (1ll << 30)) return -2;
     p.num_units = (int)units;
