@@ -519,6 +519,26 @@ def _sm_count(device):
     return torch.cuda.get_device_properties(device).multi_processor_count
 
 
+def _split_is_faster(B, Nq, Nk, Hq, Hkv, d, sms):
+    """Whether fa_decode_cross takes less than fa_fwd_cross, by estimates in us of both.
+
+    fa_fwd_cross: 256 rows (a KV head's query heads of some tokens) to an SM, a block of 128
+    keys 2.1 us, 1.75 for up to 128 rows.  fa_decode_cross: the blocks spread over all SMs,
+    1.35 us each at d = 128 and 0.8 to 1.1 at 64, 2.2 for more than 128 rows; a start and a
+    join that grow with the rows.  Over 90 sizes (1 to 150 queries, 300 and 3,000 keys, B 1 to
+    12, 8/1, 16/16 and 32/8 heads) the worse one was taken at most 5 us beside the better."""
+    group = Hq // Hkv
+    tokens = 128 // group if group <= 128 else 128
+    heads = Hkv if group <= 128 else Hq
+    rows, blocks = Nq * group, -(-Nk // 128)
+    waves = -(-B * heads * -(-Nq // (2 * tokens)) // sms)
+    whole = 8 + waves * blocks * (2.1 if Nq > tokens else 1.75)
+    pairs = -(-rows // 256)
+    each = 2.2 if rows > 128 else 1.35 if d == 128 else 0.8 if rows <= 16 else 1.1
+    start = 10 if rows <= 8 else 13 if rows <= 32 else 19
+    return start + B * Hkv * pairs * blocks * each / sms + B * Nq * Hq * 1e-3 < whole
+
+
 def _cross_shapes(q, k, v, ndim):
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, torch.bfloat16, ndim, n)
@@ -541,10 +561,9 @@ def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, ou
         scale = 1.0 / math.sqrt(d)
     out, lse, od = _out_pair(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), out_dtype, return_lse, q)
     if split_keys is None:
-        # one SM per head and 256 queries fills a quarter of the GPU or less
-        # (32 of 148: 36 us against 40; 64: 60 against 58)
-        split_keys = (od == FA_OUT_BF16 and 0 < B * Hq * -(-Nq // 256) * 4 <= _sm_count(q.get_device())
-                      and Nk < 1 << 22 and decode_cross_workspace_bytes(B, Hq, max(Hkv, 1), Nq, d) > 0)
+        split_keys = (od == FA_OUT_BF16 and 0 < Hkv and Hq % Hkv == 0 and Nk < 1 << 22
+                      and _split_is_faster(B, Nq, Nk, Hq, Hkv, d, _sm_count(q.get_device()))
+                      and decode_cross_workspace_bytes(B, Hq, Hkv, Nq, d) > 0)
     if split_keys:
         return decode_cross(q, k, v, seq_lens_k, scale, out, lse, return_lse=False, stream=stream)
     with _device_of(q, k, v, seq_lens_k, out, lse):

@@ -376,10 +376,10 @@ int fa_decode_shared(const void *q, const void *k_cache, const void *v_cache,
  * few of a speculated step, against its encoder states.  fa_fwd_cross's
  * layouts, result, treatment of rows behind seq_lens_k (which may be NULL) and
  * of lengths that do not fit, with o bf16.  The keys are split over the whole
- * GPU ("Flash-Decoding"), where fa_fwd_cross gives each 256 queries of a head
- * to one SM: the faster call while those are fewer than a quarter of the SMs
- * (B * Hq * ceil(Nq / 256); 30 queries, 16 heads, 4,000 keys 19 us against 62)
- * or Nq * Hq / Hkv is small.
+ * GPU ("Flash-Decoding"), where fa_fwd_cross gives each 256 rows of a KV head
+ * to one SM: the faster call while those leave many SMs idle and the keys are
+ * many (30 queries, 16 heads, 4,000 keys 19 us against 62), or for a few tokens
+ * (12 sequences of one, 16 heads, 3,000 keys 33 us against 94).
  *   workspace   fa_decode_cross_workspace_bytes(...) bytes, 256-byte aligned,
  *               not to be shared by calls that may overlap on the GPU.
  *   Hq / Hkv at most 128, Nq * Hq / Hkv at most 524288 (else
