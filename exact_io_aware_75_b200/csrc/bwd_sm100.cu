@@ -53,7 +53,13 @@ namespace fa {
 
 namespace bwd_impl {
 
-constexpr int kD = 128;          // tile width in d; a head dim of 64 is zero-padded to it
+// Widest head dim.  d = 64 takes one 64-column box of each tile instead of two
+// (and half the products' steps or columns); only dQ^T keeps M = 128, whose
+// lanes 64-127 multiply what lies behind the K box and are not read.  Against
+// zero-padded 128-wide tiles: 253 us for 263 (4 x 2,048 causal, 16 heads), 560
+// for 611 with the forward (packed cross attention, 24 pairs of up to 1,024 x
+// 2,048); what remains is the elementwise pass, which d does not shorten.
+constexpr int kD = 128;
 constexpr int kBlockK = 128;   // keys per unit
 constexpr int kBlockQ = 64;    // queries per tile
 constexpr int kPartQ = 16;     // queries per step of the elementwise pass
@@ -271,19 +277,20 @@ struct Shared {
 };
 static_assert(kSmemBytes + sizeof(Shared) <= 232448, "shared memory");
 
-// Cross attention: zeros over rows [valid, rows) of a tile of two 64-column
+// Cross attention: zeros over rows [valid, rows) of a tile of 64-column
 // boxes, one warp.  What lies behind a sequence's end (other sequences,
 // padding, NaN included) would otherwise meet P = 0 or dS = 0 in a product.
+template <int DH>
 __device__ __forceinline__ void clear_rows(uint8_t *tile, int rows, int valid, int box_bytes) {
     const int n16 = (rows - valid) * 8;
-    for (int b = 0; b < kD / 64; ++b)
+    for (int b = 0; b < DH / 64; ++b)
         for (int i = lane_id(); i < n16; i += 32)
             *reinterpret_cast<uint4 *>(tile + b * box_bytes + valid * 128 + i * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ------------------------------------------------------------- TMA producer
-template <bool CROSS>
+template <int DH, bool CROSS>
 __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const CUtensorMap *tmV,
                          const CUtensorMap *tmdO, const Params &p, Shared &sh, uint8_t *smem) {
     volatile int *abort = &sh.abort;
@@ -297,8 +304,8 @@ __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const C
         const bool kv_clear = CROSS && w.Lk - w.j0 < kBlockK && w.tokk0 + w.Lk < p.total_k;
         uint64_t *kv_bar = kv_clear ? &sh.kv_tail : &sh.kv_full;
         if (lane == 0) {
-            mbar_arrive_expect_tx(kv_bar, 2 * kKVTile);
-            for (int b = 0; b < kD / 64; ++b) {
+            mbar_arrive_expect_tx(kv_bar, 2 * kBlockK * DH * 2);
+            for (int b = 0; b < DH / 64; ++b) {
                 tma_load_3d(smem + kOffK + b * kKVBox, tmK, kv_bar, b * 64, w.kvh, w.tokk0 + w.j0);
                 tma_load_3d(smem + kOffV + b * kKVBox, tmV, kv_bar, b * 64, w.kvh, w.tokk0 + w.j0);
             }
@@ -307,8 +314,8 @@ __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const C
         if (kv_clear) {
             ++kv_tails;
             if (!mbar_wait_warp(&sh.kv_tail, (kv_tails - 1) & 1, abort)) goto out;
-            clear_rows(smem + kOffK, kBlockK, w.Lk - w.j0, kKVBox);
-            clear_rows(smem + kOffV, kBlockK, w.Lk - w.j0, kKVBox);
+            clear_rows<DH>(smem + kOffK, kBlockK, w.Lk - w.j0, kKVBox);
+            clear_rows<DH>(smem + kOffV, kBlockK, w.Lk - w.j0, kKVBox);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.kv_full);
@@ -322,8 +329,8 @@ __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const C
             const bool qd_clear = CROSS && w.L - q0 < kBlockQ && w.tok0 + w.L < p.total_tokens;
             uint64_t *qd_bar = qd_clear ? &sh.qd_tail : &sh.qd_full[s];
             if (lane == 0) {
-                mbar_arrive_expect_tx(qd_bar, 2 * kQTile);
-                for (int b = 0; b < kD / 64; ++b) {
+                mbar_arrive_expect_tx(qd_bar, 2 * kBlockQ * DH * 2);
+                for (int b = 0; b < DH / 64; ++b) {
                     tma_load_3d(st + b * kQBox, tmQ, qd_bar, b * 64, h, w.tok0 + q0);
                     tma_load_3d(st + kQTile + b * kQBox, tmdO, qd_bar, b * 64, h, w.tok0 + q0);
                 }
@@ -346,8 +353,8 @@ __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const C
             if (qd_clear) {
                 ++qd_tails;
                 if (!mbar_wait_warp(&sh.qd_tail, (qd_tails - 1) & 1, abort)) goto out;
-                clear_rows(st, kBlockQ, w.L - q0, kQBox);
-                clear_rows(st + kQTile, kBlockQ, w.L - q0, kQBox);
+                clear_rows<DH>(st, kBlockQ, w.L - q0, kQBox);
+                clear_rows<DH>(st + kQTile, kBlockQ, w.L - q0, kQBox);
                 fence_proxy_async_smem();
             }
             __syncwarp();
@@ -374,7 +381,7 @@ out:
 // of tile n overwrites the P^T that dV of tile n-2 reads, so it waits for
 // that MMA to complete; dP^T overwrites the dQ^T of tile n-2, so it waits
 // until that is drained.
-template <bool CROSS>
+template <int DH, bool CROSS>
 __device__ void mma_issuer_s(const Params &p, Shared &sh, uint8_t *smem) {
     volatile int *abort = &sh.abort;
     const uint32_t tmem = sh.tmem_base;
@@ -396,7 +403,7 @@ __device__ void mma_issuer_s(const Params &p, Shared &sh, uint8_t *smem) {
             const uint32_t qLo = desc_lo(aStage + s * kStageBytes, 16);
             const uint32_t dLo = qLo + (kQTile >> 4);
             #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
+            for (int ks = 0; ks < DH / 16; ++ks) {
                 const uint32_t okv = ((ks >> 2) * kKVBox + (ks & 3) * 32) >> 4;
                 const uint32_t oq = ((ks >> 2) * kQBox + (ks & 3) * 32) >> 4;
                 mma_ss_lo(tmem + kColS + b * kBlockQ, kLo + okv, qLo + oq, idS, ks > 0);
@@ -404,7 +411,7 @@ __device__ void mma_issuer_s(const Params &p, Shared &sh, uint8_t *smem) {
             if (n >= 2 && !mbar_wait(&sh.dq_free[b], ((n - 2) >> 1) & 1, abort)) goto out;
             tc_fence_after();
             #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
+            for (int ks = 0; ks < DH / 16; ++ks) {
                 const uint32_t okv = ((ks >> 2) * kKVBox + (ks & 3) * 32) >> 4;
                 const uint32_t oq = ((ks >> 2) * kQBox + (ks & 3) * 32) >> 4;
                 mma_ss_lo(tmem + kColDP + b * kBlockQ, vLo + okv, dLo + oq, idS, ks > 0);
@@ -427,11 +434,11 @@ out:
 // per step, boxes of 64 columns LBO apart); dS^T sits in shared memory as 128
 // key rows of 64 queries, 128-byte swizzled: K-major A for dK, MN-major B
 // for dQ^T.
-template <bool CROSS>
+template <int DH, bool CROSS>
 __device__ void mma_issuer_grad(const Params &p, Shared &sh, uint8_t *smem) {
     volatile int *abort = &sh.abort;
     const uint32_t tmem = sh.tmem_base;
-    const uint32_t idAcc = idesc_bf16_f32_ab(kBlockK, kD, false, true);
+    const uint32_t idAcc = idesc_bf16_f32_ab(kBlockK, DH, false, true);
     const uint32_t idDQ = idesc_bf16_f32_ab(kD, kBlockQ, true, true);
     const uint32_t kLoMN = desc_lo(smem_u32(smem + kOffK), kKVBox);
     const uint32_t aStage = smem_u32(smem + kOffStage), aDS = smem_u32(smem + kOffDS);
@@ -624,11 +631,11 @@ __device__ void softmax_wg(const Params &p, Shared &sh, uint8_t *smem) {
         const uint32_t tAcc = sh.tmem_base + lanes + (wg ? kColDK : kColDV);
         const float mul = wg ? p.scale : 1.f;
         #pragma unroll
-        for (int c = 0; c < kD; c += 32) {
+        for (int c = 0; c < DH; c += 32) {
             uint32_t v[32];
             tmem_ld32(tAcc + c, v);
             tmem_wait_ld();
-            if (key_ok && c < DH) {   // columns past a 64-wide head are padding
+            if (key_ok) {
                 uint4 *d4 = reinterpret_cast<uint4 *>(dst + c);
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -768,11 +775,11 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     } else {
         regs_decrease<kRegsControl>();
         if (warp == kWarpTma) {
-            producer<CROSS>(&tmQ, &tmK, &tmV, &tmdO, p, sh, smem);
+            producer<DH, CROSS>(&tmQ, &tmK, &tmV, &tmdO, p, sh, smem);
         } else if (warp == kWarpMma) {
-            if (lane_id() == 0) mma_issuer_s<CROSS>(p, sh, smem);
+            if (lane_id() == 0) mma_issuer_s<DH, CROSS>(p, sh, smem);
         } else if (warp == kWarpMmaGrad) {
-            if (lane_id() == 0) mma_issuer_grad<CROSS>(p, sh, smem);
+            if (lane_id() == 0) mma_issuer_grad<DH, CROSS>(p, sh, smem);
         }
     }
     __syncwarp();
@@ -933,10 +940,7 @@ int launch_bwd(const BwdArgs &a, cudaStream_t stream) {
         if (cudaGetLastError() != cudaSuccess) return -5;
     }
 
-    // Tensors are dh wide; tiles are kD = 128 wide, loaded as two 64-column
-    // boxes.  With dh = 64 the second box lies wholly past the tensor's inner
-    // extent, and TMA fills it with zeros: the padded columns add nothing to
-    // S or dP, and their dK, dV, dQ columns are never written.
+    // Tiles are loaded in 64-column boxes: two of them for dh = 128, one for 64.
     alignas(64) CUtensorMap tq, tk, tv, tdo, tdq;
     const uint64_t T = (uint64_t)total;
     // (without any key the K and V maps are never used: any valid address)

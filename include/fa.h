@@ -191,8 +191,7 @@ int fa_fwd_varlen_sinks(const void *q, const void *k, const void *v, void *o, fl
  *   workspace  device scratch of at least fa_bwd_workspace_bytes(B * N, Hq, d)
  *              bytes, 256-byte aligned; contents on entry do not matter; not
  *              to be shared by calls that may overlap on the GPU.
- *   causal, window, scale as for fa_fwd.  d = 64 or 128 (a head dim of 64 is
- *   computed on 128-wide tiles with zero padding, at the cost of 128).
+ *   causal, window, scale as for fa_fwd.  d = 64 or 128.
  *   N == 0 or B == 0 is a no-op returning FA_OK.
  * dQ is accumulated in fp32 with atomic adds, so its last bits may differ
  * from run to run; dK and dV are deterministic.
