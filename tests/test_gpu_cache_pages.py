@@ -249,6 +249,46 @@ def test_collect_and_compact_bad_inputs(fa):
     assert sorted([table_out[0, 0].item(), table_out[1, 1].item(), table_out[1, 2].item()]) == [0, 1, 2]
 
 
+@pytest.mark.parametrize("lens,pages,width", [
+    ([16 * 700, 0, 16 * 257, 16 * 256 + 1], 1500, 700), ([40] * 128, 32768, 256), ([40] * 129, 32768, 256),
+    ([16 * 300] * 3, 32769, 300), ([33] * 500, 3000, 513), ([33] * 40, 3000, 768), ([700] * 64, 3000, 512),
+])
+def test_many_table_entries(fa, lens, pages, width):
+    b = batch(lens, pages, 1, 64, seed=14, width=width)
+    dev = Dev(b)
+    free = torch.full((pages,), -3, dtype=torch.int32, device="cuda")
+    c = Cache(b["k"], b["v"], b["table"], lens)
+    want = c.collect()
+    fa.cache_collect(dev.table, dev.lens, free, dev.count_out)
+    assert fa.check_device_error() == 0
+    assert dev.count_out.tolist() == [len(want)]
+    assert free.tolist() == want + [-3] * (pages - len(want))
+    table_out = torch.full_like(dev.table, -9)
+    free.fill_(-3)
+    fa.cache_compact(dev.k, dev.v, dev.table, dev.lens, table_out, free, dev.count_out)
+    assert fa.check_device_error() == 0
+    want_table = torch.full_like(b["table"], -9)
+    left = c.compact(want_table)
+    assert torch.equal(table_out.cpu(), want_table)
+    assert free.tolist() == left + [-3] * (pages - len(left))
+    assert dev.same_cache(c)
+
+
+@pytest.mark.parametrize("pages", [12, 40000])
+def test_bad_entries_and_lengths_are_not_in_use(fa, pages):
+    b = batch([20, 40, 16], 12, 1, 64, seed=15)
+    b["table"][0, 1] = pages
+    b["table"][1, 0] = -1
+    lens = i32([20, 40, 16 * b["table"].shape[1] + 1])     # the last cannot be: read as 0
+    used = {int(b["table"][0, 0]), int(b["table"][1, 1]), int(b["table"][1, 2])}
+    free = torch.full((pages,), -3, dtype=torch.int32, device="cuda")
+    count = i32([-1])
+    fa.cache_collect(b["table"].cuda(), lens, free, count)
+    assert fa.check_device_error() == fa.FA_ERR_INVALID_ARG
+    assert free.tolist() == [p for p in range(pages - 1, -1, -1) if p not in used] + [-3] * 3
+    assert count.tolist() == [pages - 3]
+
+
 @pytest.mark.parametrize("Hkv,d,fp8", [(8, 128, False), (1, 64, True)])
 def test_copy_pages(fa, Hkv, d, fp8):
     b = batch([1], 60, Hkv, d, seed=11, fp8=fp8)
