@@ -28,6 +28,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import inspect
 import math
 import os
 
@@ -191,6 +192,30 @@ def _stream(stream=None):
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _on_stream(f):
+    """f(..., stream=s) as f(...) inside torch.cuda.stream(s), so that what f allocates (its
+    workspace, outputs not passed) belongs to s: in the pool of the caller's stream a
+    workspace could be handed out again while the kernels on s still use it."""
+    names = list(inspect.signature(f).parameters)
+    first, at = names[0], names.index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return f(*args, **kwargs)
+        x = args[0] if args else kwargs.get(first)
+        if isinstance(x, torch.Tensor) and x.is_cuda and x.device != stream.device:
+            raise FAError(FA_ERR_INVALID_ARG, f"a stream of {stream.device}, {first} on {x.device}")
+        if len(args) > at:
+            args = args[:at] + (None,) + args[at + 1:]
+        else:
+            kwargs["stream"] = None
+        with torch.cuda.stream(stream):
+            return f(*args, **kwargs)
+    return call
 
 
 def _check(rc: int, where: str):
@@ -546,6 +571,7 @@ def _cross_shapes(q, k, v, ndim):
         raise FAError(FA_ERR_INVALID_ARG, "q/k/v shape")
 
 
+@_on_stream
 def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, out=None, lse=None,
               return_lse=True, stream=None, split_keys=None):
     """Cross attention, dense.  q [B,Nq,Hq,d], k/v [B,Nk,Hkv,d] bf16, seq_lens_k [B] int32
@@ -573,6 +599,7 @@ def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, ou
     return out, lse
 
 
+@_on_stream
 def fwd_varlen_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale=None,
                      out_dtype=torch.bfloat16, out=None, lse=None, return_lse=True, stream=None):
     """Cross attention, packed.  q [Tq,Hq,d], k/v [Tk,Hkv,d] bf16, cu_seqlens_q and
@@ -595,6 +622,7 @@ def fwd_varlen_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
     return out, lse
 
 
+@_on_stream
 def bwd_cross(q, k, v, o, dout, lse, seq_lens_k=None, scale=None, dq=None, dk=None, dv=None,
               workspace=None, stream=None):
     """Backward of fwd_cross.  q/o/dout [B,Nq,Hq,d], k/v [B,Nk,Hkv,d] bf16, lse [B,Hq,Nq]
@@ -623,6 +651,7 @@ def bwd_cross(q, k, v, o, dout, lse, seq_lens_k=None, scale=None, dq=None, dk=No
     return dq, dk, dv
 
 
+@_on_stream
 def bwd_varlen_cross(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                      scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Backward of fwd_varlen_cross.  q/o/dout [Tq,Hq,d], k/v [Tk,Hkv,d] bf16, lse [Hq,Tq]
@@ -657,6 +686,7 @@ def decode_shared_workspace_bytes(num_seqs, Hq, Hkv, d) -> int:
     return int(_lib.fa_decode_shared_workspace_bytes(int(num_seqs), int(Hq), int(Hkv), int(d)))
 
 
+@_on_stream
 def decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, scale=None,
                   sinks=None, out=None, lse=None, return_lse=True, workspace=None, stream=None):
     """Paged decode of sequences that share prefixes.  q [S,Hq,d], caches [P,16,Hkv,d],
@@ -700,6 +730,7 @@ def decode_cross_workspace_bytes(B, Hq, Hkv, Nq, d) -> int:
     return int(_lib.fa_decode_cross_workspace_bytes(int(B), int(Hq), int(Hkv), int(Nq), int(d)))
 
 
+@_on_stream
 def decode_cross(q, k, v, seq_lens_k=None, scale=None, out=None, lse=None, return_lse=True,
                  workspace=None, stream=None):
     """Cross attention of few queries, the keys split over the GPU.  q [B,Nq,Hq,d], k/v
@@ -962,6 +993,7 @@ def cache_collect_workspace_bytes(num_pages) -> int:
     return int(_lib.fa_cache_collect_workspace_bytes(int(num_pages)))
 
 
+@_on_stream
 def cache_collect(block_table, seq_lens, free_pages, free_count, page_size=16, workspace=None,
                   stream=None):
     """The pages that no sequence uses, descending, into free_pages [P] and free_count [1]
@@ -985,6 +1017,7 @@ def cache_compact_workspace_bytes(num_pages) -> int:
     return int(_lib.fa_cache_compact_workspace_bytes(int(num_pages)))
 
 
+@_on_stream
 def cache_compact(k_cache, v_cache, block_table, seq_lens, block_table_out, free_pages, free_count,
                   k_scale=None, v_scale=None, workspace=None, stream=None):
     """Moves the pages in use to the cache's front.  caches [P,16,Hkv,d] (bf16, or E4M3 with

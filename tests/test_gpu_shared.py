@@ -363,3 +363,31 @@ def test_cross_bad_length(fa):
     fa.decode_cross(t, k, k, i32([-1, 41, 40]), out=o, lse=lse)
     assert fa.check_device_error() == fa.FA_ERR_INVALID_ARG
     assert (o[:2] == 5).all() and (lse[:2] == 5).all() and (o[2] == 1).all()
+
+
+def test_a_stream_passed_owns_the_workspace(fa):
+    """The call's workspace is not handed out to the caller's stream while the given one still needs it."""
+    b = Batch([500 + 9 * i for i in range(12)], [(0, 12)], [490], 8, 2, 64, seed=23)
+    dev = [t.cuda() for t in (b.q, b.k, b.v, b.table)] + [i32(b.lens), i32([0, 12]), i32([490])]
+    need = fa.decode_shared_workspace_bytes(12, 8, 2, 64)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    o, lse = fa.decode_shared(*dev, stream=side)
+    trash = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (need, need) + (o.nbytes, lse.nbytes) * 2]
+    torch.cuda.synchronize()
+    assert fa.check_device_error() == 0 and len(trash) == 6
+    b.check(o, lse)
+
+
+def test_stream_forms(fa):
+    """By position, by name, none: one result."""
+    q, k = (torch.randn(s, device="cuda").to(torch.bfloat16) for s in ((2, 5, 8, 64), (2, 300, 2, 64)))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [fa.decode_cross(q, k, k), fa.decode_cross(q, k, k, None, None, None, None, True, None, side),
+           fa.decode_cross(q, k, k, stream=side), fa.decode_cross(q=q, k=k, v=k, stream=side)]
+    torch.cuda.synchronize()
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])

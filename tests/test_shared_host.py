@@ -66,3 +66,25 @@ def test_binding_refuses(fa):
         fa.decode_shared(t, t[None], t[None], i[None], i, i, i)          # not CUDA tensors
     with pytest.raises(fa.FAError):
         fa.decode_cross(t[None], t[None], t[None])
+
+
+def test_stream_argument(fa):
+    """A stream of another device is refused; the calls keep their signatures."""
+    import inspect
+    for f in (fa.fwd_cross, fa.fwd_varlen_cross, fa.bwd_cross, fa.bwd_varlen_cross, fa.decode_shared, fa.decode_cross,
+              fa.cache_collect, fa.cache_compact):
+        assert inspect.signature(f).parameters["stream"].default is None
+
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cuda", 0)
+
+    q = torch.zeros(1, 1, 8, 64, dtype=torch.bfloat16).as_subclass(OnGpu)
+    for call in (lambda: fa.decode_cross(q, q, q, stream=Stream()), lambda: fa.decode_cross(q=q, k=q, v=q, stream=Stream()),
+                 lambda: fa.decode_cross(q, q, q, None, None, None, None, True, None, Stream())):
+        with pytest.raises(fa.FAError, match="stream"):
+            call()
