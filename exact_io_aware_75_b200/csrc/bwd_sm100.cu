@@ -61,8 +61,9 @@ namespace bwd_impl {
 // K and V below 343.  d = 64 also has the tensor memory for a third tile in
 // flight, or for a second set of dV and dK to let a unit's last rows be written
 // behind the next one's first tile: 359 and 377, so neither is done.  What
-// bounds a tile is the elementwise pass, which d does not shorten (1.2 us for
-// 1.5 at d = 128).
+// bounds a tile is its way through the five products and the elementwise pass
+// between them: of 4,700 cycles for a warpgroup's tile the pass takes 1,930,
+// the wait for the next S^T the rest.
 constexpr int kD = 128;
 constexpr int kBlockK = 128;   // keys per unit
 constexpr int kBlockQ = 64;    // queries per tile
@@ -321,6 +322,28 @@ __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const C
     FOR_EACH_BWD_UNIT(u) {
         Unit w;
         if (!get_unit<CROSS>(u, p, w)) continue;
+        // LSE and D of a tile's rows, asked for a tile ahead: with their latency in
+        // each step this warp set the ring's pace (S^T waited 500 cycles a tile for
+        // Q and dO at d = 64, 1,100 at 128; now 110 and 710).  8 x 2,048, 16
+        // heads, d = 64: 760 to 600 us, causal 430 to 348; 4,096, 32/8 heads,
+        // d = 128: 747 to 718 with the two small kernels, causal 391 to 384.
+        float next_l[2], next_d[2];
+        auto ask_rows = [&](int k) {
+            int h, q0;
+            tile_of(w, p, k, h, q0);
+            #pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = q0 + lane + 32 * e;
+                next_l[e] = INFINITY;
+                next_d[e] = 0.f;
+                if (i < w.L) {
+                    const size_t idx = row_index(p, w, h, i);
+                    next_l[e] = __ldg(p.lse + idx);
+                    next_d[e] = __ldg(p.dd + idx);
+                }
+            }
+        };
+        ask_rows(0);
         const int set = uc % kSets<DH>;
         uint8_t *tK = smem + kOffK + set * kKVBox, *tV = smem + kOffV + set * kKVBox;
         if (!mbar_wait_warp(&sh.kv_empty[set], ((uc / kSets<DH>) & 1) ^ 1, abort)) goto out;
@@ -361,17 +384,12 @@ __device__ void producer(const CUtensorMap *tmQ, const CUtensorMap *tmK, const C
             // The tile's -LSE (log2 units) and -D; rows past the sequence get
             // LSE = +inf, so their P is exactly 0.
             float *rs = rows + s * 2 * kBlockQ;
+            const float l[2] = {next_l[0], next_l[1]}, dv[2] = {next_d[0], next_d[1]};
+            if (k + 1 < w.ntiles) ask_rows(k + 1);
             #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int rr = lane + 32 * e, i = q0 + rr;
-                float l2 = INFINITY, dv = 0.f;
-                if (i < w.L) {
-                    const size_t idx = row_index(p, w, h, i);
-                    l2 = __ldg(p.lse + idx) * 1.4426950408889634f;
-                    dv = __ldg(p.dd + idx);
-                }
-                rs[rr] = -l2;
-                rs[kBlockQ + rr] = -dv;
+                rs[lane + 32 * e] = -(l[e] * 1.4426950408889634f);
+                rs[kBlockQ + lane + 32 * e] = -dv[e];
             }
             if (qd_clear) {
                 ++qd_tails;
