@@ -128,6 +128,9 @@ struct Params {
 
 struct Shared {
     uint64_t q_full[2];
+    // A wait knows a phase by its parity alone.  A warp that skips uses of a slot
+    // (an issuer, the V tiles of the other's shares) may wait for a later one only
+    // after something that implies that all earlier ones are over.
     uint64_t kv_full[8], kv_empty[8], tail;
     uint64_t s_full[2], p_lo[2], p_hi[2], o_full[2];
     uint64_t st_full[2][kSBufs], st_empty[2][kSBufs], pt_full[2][2], pt_empty[2][2];
@@ -720,8 +723,10 @@ __device__ void mma_issuer_pv(const Params &p, const Table &tab, Shared &sh, uin
             const int vs = it % C::kStages;
             const uint32_t c = cnt[w.wg]++;
             const int b = c & 1;
-            if (!mbar_wait_warp(&sh.kv_full[vs], (it / C::kStages) & 1, abort)) goto out;
+            // P first: it comes from a warpgroup that has left the shares before,
+            // so that V's earlier uses of the slot (of shares skipped above) are over
             if (!mbar_wait_warp(&sh.pt_full[w.wg][b], (c >> 1) & 1, abort)) goto out;
+            if (!mbar_wait_warp(&sh.kv_full[vs], (it / C::kStages) & 1, abort)) goto out;
             tc_fence_after();
             if (elect_one()) {
                 const uint32_t pt = desc_lo(smem_u32(sQ + w.wg * C::kQBytes + few_p(b)), 16);
