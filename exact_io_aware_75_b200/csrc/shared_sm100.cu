@@ -652,8 +652,9 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
             continue;
         }
         bool first[2] = {true, true};
+        const bool one = !w.pair && nb == 1;
         for (int t = 0; t < 2; ++t) {
-            if (t == 1 && !w.pair && nb == 1) continue;
+            if (t == 1 && one) continue;
             if (!mbar_wait_warp(&sh.q_full[t], q_uses[t] & 1, abort)) goto out;
             ++q_uses[t];
         }
@@ -687,6 +688,12 @@ __device__ void mma_issuer(const Params &p, const Table &tab, Shared &sh, uint8_
             prev_use = v_use;
         }
         const int t = w.pair ? 1 : (nb - 1) & 1;
+        if (one) {
+            // of one block the second warpgroup has no tile, but its shares before, and
+            // with them their uses of V's slot, are to be over: it says so on its Q
+            if (!mbar_wait_warp(&sh.q_full[1], q_uses[1] & 1, abort)) goto out;
+            ++q_uses[1];
+        }
         if (!w.pair) {
             if (!mbar_wait_warp(&sh.kv_full[prev_v], prev_use & 1, abort)) goto out;
             tc_fence_after();
@@ -1109,9 +1116,9 @@ __device__ void softmax_wg(const Params &p, const Table &tab, Shared &sh, uint8_
                 *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBoxBytes + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
             fence_proxy_async_smem();
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full[t]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[t]);        // (without a tile: this share has begun)
         Row row{-INFINITY, 0.f};
         for (int j = j0; j < w.kb1 && ok; j += step) {
             ok = mbar_wait_warp(&sh.s_full[t], cnt.s & 1, &sh.abort);

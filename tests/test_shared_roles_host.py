@@ -319,6 +319,15 @@ def test_few_rows_after_many():
             check(items, 1, d, late, pv_first, both_q)
 
 
+def test_one_block_of_many_rows_after_few():
+    """One block of many rows while the other warpgroup still has few rows whose V is late."""
+    pv_first, both_q = from_source()
+    late = ["K", "kin", "S", "0", "1", "mma", "PV", "V", "vin"]
+    for d in (64, 128):
+        for keys in range(100, 1500, 100):
+            check([(8, 90), (8, keys), (48, 100)], 1, d, late, pv_first, both_q)
+
+
 def test_the_model_finds_a_wait_too_early():
     """V asked for before P: the model has to show it."""
     rng = random.Random(2)
