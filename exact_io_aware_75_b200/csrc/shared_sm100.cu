@@ -100,15 +100,23 @@ struct Cfg {
 };
 
 // The plan, in shared memory.
+constexpr int kSlotBits = 20;
+static_assert(kRows * (kMaxItems + kSharedMaxCtas) < 1 << kSlotBits && kMaxItems < 1 << (32 - kSlotBits),
+              "partial rows and items in a word");
 struct Table {
-    int start[kMaxItems];            // cost before the item
-    int slot[kMaxItems];             // partial rows before the item
+    int start[kMaxItems + 1];        // cost before the item; INT_MAX behind the last
+    // partial rows before the item, and from kSlotBits on how many items on the next
+    // one with keys (or the end) is
+    uint32_t slot[kMaxItems];
+    uint32_t some[kMaxItems / 32];   // a bit per item: it has keys
     uint32_t gi[kMaxGroupItems];     // group items: group | row pair << 16
     uint16_t cu[kMaxSeqs + 2];       // first sequence of each group
     int own[kMaxSeqs];               // pages of each sequence that its group reads
     int keys[kMaxSeqs];              // keys behind them (not paged: all keys)
     int num_group_items, num_items, span;
+    int first;                       // this CTA's first item << 8 | share of it (INT_MAX: none)
 };
+static_assert(kSharedMaxCtas <= 256, "shares of an item in 8 bits");
 
 struct Params {
     const uint16_t *q;
@@ -337,7 +345,10 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     if (tid == 0) {
         tab.num_group_items = ni;
         tab.num_items = N;
+        tab.first = INT_MAX;
+        tab.start[N] = INT_MAX;
     }
+    if (tid < kMaxItems / 32) tab.some[tid] = 0;
     __syncthreads();
     // cost before each item; a thread has `per` consecutive ones
     const int per = ceil_div(N, kThreads), i0 = min(N, tid * per), i1 = min(N, i0 + per);
@@ -355,6 +366,7 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     const int most = p.S * p.Nq * p.G > kBlockM ? p.cost_pair : p.cost_one;
     const int span = max(most, ceil_div(total, p.n));
     const uint32_t inv = 0xffffffffu / (uint32_t)span;
+    const int share = blockIdx.x / p.Hkv, lo = share * span;
     int rows = 0;
     #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
@@ -363,10 +375,13 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
         tab.start[i] = start;
         int parts = 0;
         if (w.keys > 0) {
+            atomicOr(&tab.some[i >> 5], 1u << (i & 31));
             const int last = start + (ceil_div(w.keys, kBlockN) - 1) * block_cost(p, w.rows);
-            parts = div_span(last, span, inv) - div_span(start, span, inv) + 1;
+            const int s0 = div_span(start, span, inv);
+            parts = div_span(last, span, inv) - s0 + 1;
+            if (last >= lo && start < lo + span) atomicMin(&tab.first, i << 8 | (share - s0));
         }
-        tab.slot[i] = rows;
+        tab.slot[i] = (uint32_t)rows;
         if (lead) p.items[i] = make_int4(0, parts, w.rows, 0);
         rows += parts * w.rows;
     }
@@ -374,8 +389,17 @@ __device__ void make_plan(const Params &p, Table &tab, int *scratch, int *s_warp
     const int slot0 = block_scan(rows, s_warp, all);
     #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-        tab.slot[i] += slot0;
-        if (lead) p.items[i].x = tab.slot[i];
+        const int slot = (int)tab.slot[i] + slot0;
+        if (lead) p.items[i].x = slot;
+        int next = i + 1;
+        uint32_t later = next < N ? tab.some[next >> 5] >> (next & 31) : 1u;
+        #pragma unroll 1
+        while (!later) {
+            next = (next | 31) + 1;
+            later = next < N ? tab.some[next >> 5] : 1u;
+        }
+        next = min(N, next + __ffs(later) - 1);
+        tab.slot[i] = (uint32_t)slot | (uint32_t)(next - i) << kSlotBits;
     }
     if (tid == 0) tab.span = span;
     __syncthreads();
@@ -394,45 +418,31 @@ struct Work {
 };
 
 struct Walker {
-    int i, lo, hi, items, groups, part, turn;   // part: of the first item, whose blocks may begin before lo
+    int i, lo, hi, groups, turn;
+    int part;       // of the first item, whose blocks may begin before lo; 0 of the others
     uint32_t ring;
     __device__ __forceinline__ void begin(const Params &p, const Table &tab) {
-        const int share = blockIdx.x / p.Hkv, span = tab.span;
         turn = 0;
         ring = 0;
-        items = tab.num_items;
         groups = tab.num_group_items;
-        lo = share * span;
-        hi = lo + span;
-        int a = 0, b = items;                  // the last item that starts at or before lo
-        #pragma unroll 1
-        while (b - a > 1) {
-            const int mid = (a + b) >> 1;
-            if (tab.start[mid] <= lo) a = mid; else b = mid;
-        }
-        i = a;
-        part = share - tab.start[a] / span;
+        lo = blockIdx.x / p.Hkv * tab.span;
+        hi = lo + tab.span;
+        i = min(tab.first >> 8, tab.num_items);
+        part = tab.first & 255;
     }
     template <bool PAGED>
     __device__ __forceinline__ bool next(const Params &p, const Table &tab, Work &w) {
-        bool found = false;
-        #pragma unroll 1
-        while (!found && i < items) {
-            // (the compiler must not carry the table's values from turn to turn:
-            // without this a build skipped every item after an empty one)
-            asm volatile("" ::: "memory");
-            const int start = tab.start[i];
-            if (start >= hi) break;
-            w.it = get_item<PAGED>(p, tab, groups, i);
-            const int cost = block_cost(p, w.it.rows), nb = ceil_div(w.it.keys, kBlockN);
-            w.kb0 = start >= lo ? 0 : min(nb, div_cost(lo - start, cost));
-            w.kb1 = min(nb, div_cost(hi - start, cost));
-            w.slot = tab.slot[i] + part * w.it.rows;
-            found = w.kb0 < w.kb1;
-            ++i;
-            part = 0;
-        }
-        if (!found) return false;
+        // (the plan says which item with keys comes next: no loop here over those without)
+        const int start = tab.start[i];
+        if (start >= hi) return false;
+        const uint32_t slot = tab.slot[i];
+        w.it = get_item<PAGED>(p, tab, groups, i);
+        const int cost = block_cost(p, w.it.rows), nb = ceil_div(w.it.keys, kBlockN);
+        w.kb0 = start >= lo ? 0 : min(nb, div_cost(lo - start, cost));
+        w.kb1 = min(nb, div_cost(hi - start, cost));
+        w.slot = (int)(slot & ((1u << kSlotBits) - 1u)) + part * w.it.rows;
+        i += slot >> kSlotBits;
+        part = 0;
         w.pair = w.it.rows > kBlockM;
         w.few = w.it.rows <= kFewRows;
         w.wg = turn;
