@@ -5,6 +5,8 @@ device pointers, sizes and the current CUDA stream to the C ABI declared in
 ``include/fa.h``, and raises :class:`FAError` on a non-zero status.  All
 arithmetic runs in the library's kernels.  There is no fallback: if the
 shared library is missing or fails to load, importing this package raises.
+With ``stream=s`` a call runs inside ``torch.cuda.stream(s)``, what it allocates
+included; a stream of another device than the tensors' is refused.
 
 Functions mirror the C entry points:
     fwd            -> fa_fwd            (dense prefill)
@@ -207,6 +209,8 @@ def _on_stream(f):
         if stream is None:
             return f(*args, **kwargs)
         x = args[0] if args else kwargs.get(first)
+        if isinstance(x, dict):                  # fp8_prepare's operands
+            x = next(iter(x.values()), None)
         if isinstance(x, torch.Tensor) and x.is_cuda and x.device != stream.device:
             raise FAError(FA_ERR_INVALID_ARG, f"a stream of {stream.device}, {first} on {x.device}")
         if len(args) > at:
@@ -240,6 +244,7 @@ def _need(t, dtype, ndim, name):
         raise FAError(FA_ERR_INVALID_ARG, f"{name} must be contiguous")
 
 
+@_on_stream
 def fwd(q, k, v, causal=False, window=0, scale=None, out_dtype=torch.bfloat16,
         out=None, lse=None, return_lse=True, stream=None, sinks=None, doc_ids=None,
         sink_tokens=None):
@@ -295,6 +300,7 @@ def fp8_workspace_bytes(B, N, Hkv) -> int:
     return int(_lib.fa_fp8_workspace_bytes(int(B), int(N), int(Hkv)))
 
 
+@_on_stream
 def fp8_prepare(q, k, v, signs=None, out=None, workspace=None, stream=None):
     """E4M3 operands of the FP8 prefill.  q [B,N,Hq,128], k/v [B,N,Hkv,128] bf16;
     signs fp32 [128] of +-1 (device) or None (no rotation).  Returns a dict with
@@ -332,6 +338,7 @@ def fp8_prepare(q, k, v, signs=None, out=None, workspace=None, stream=None):
     return out
 
 
+@_on_stream
 def fwd_fp8(prep, causal=False, window=0, scale=None, out_dtype=torch.bfloat16, out=None,
             lse=None, return_lse=True, stream=None):
     """FP8 prefill on fp8_prepare's operands -> (O [B,N,Hq,128], LSE [B,Hq,N])."""
@@ -357,6 +364,7 @@ def fwd_fp8(prep, causal=False, window=0, scale=None, out_dtype=torch.bfloat16, 
     return out, lse
 
 
+@_on_stream
 def fwd_varlen(q, k, v, cu_seqlens, max_seqlen, causal=False, window=0, scale=None,
                out_dtype=torch.bfloat16, out=None, lse=None, return_lse=True, stream=None,
                sinks=None, sink_tokens=None):
@@ -399,6 +407,7 @@ def fwd_varlen(q, k, v, cu_seqlens, max_seqlen, causal=False, window=0, scale=No
     return out, lse
 
 
+@_on_stream
 def fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k, max_seqlen_q,
               causal=True, window=0, scale=None, sinks=None, out_dtype=torch.bfloat16, out=None,
               lse=None, return_lse=True, stream=None):
@@ -434,6 +443,7 @@ def bwd_workspace_bytes(total_tokens, Hq, d) -> int:
     return int(_lib.fa_bwd_workspace_bytes(int(total_tokens), int(Hq), int(d)))
 
 
+@_on_stream
 def bwd(q, k, v, o, dout, lse, causal=False, window=0, scale=None, dq=None, dk=None, dv=None,
         workspace=None, stream=None, sinks=None, dsinks=None):
     """Dense backward.  q/o/dout [B,N,Hq,d], k/v [B,N,Hkv,d] bf16, lse [B,Hq,N] fp32
@@ -473,6 +483,7 @@ def bwd(q, k, v, o, dout, lse, causal=False, window=0, scale=None, dq=None, dk=N
     return dq, dk, dv
 
 
+@_on_stream
 def bwd_varlen(q, k, v, o, dout, lse, cu_seqlens, max_seqlen, causal=False, window=0,
                scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Packed backward.  q/o/dout [T,Hq,d], k/v [T,Hkv,d], lse [Hq,T], cu_seqlens [S+1]
@@ -758,6 +769,7 @@ def decode_workspace_bytes(num_seqs, Hq, d, page_size, max_pages_per_seq) -> int
                                               int(max_pages_per_seq)))
 
 
+@_on_stream
 def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None, lse=None,
                  return_lse=True, workspace=None, stream=None, sinks=None):
     """Paged decode.  q [S,Hq,d], caches [P,ps,Hkv,d], block_table [S,maxp] int32,
@@ -796,6 +808,7 @@ def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=Non
     return out, lse
 
 
+@_on_stream
 def decode_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, scale=None,
                      sinks=None, out=None, lse=None, return_lse=True, workspace=None,
                      stream=None):
@@ -833,6 +846,7 @@ def decode_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
     return out, lse
 
 
+@_on_stream
 def decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None,
                          lse=None, return_lse=True, stream=None):
     """Paged decode with the library's fixed device scratch instead of a
@@ -912,6 +926,7 @@ def _bytes_of(workspace, need, like):
     return workspace
 
 
+@_on_stream
 def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, free_count,
                block_table_out, seq_lens_out, free_count_out, k_scale=None, v_scale=None,
                stream=None):
@@ -944,6 +959,7 @@ def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, fre
                                   _stream(stream)), "fa_cache_fork")
 
 
+@_on_stream
 def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, free_pages,
                  free_count, seq_lens_out, free_count_out, stream=None):
     """New tokens behind the sequences' ends.  k_new, v_new [T,Hkv,d] bf16 packed by cu_new
@@ -977,6 +993,7 @@ def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, 
                "fa_cache_append")
 
 
+@_on_stream
 def cache_copy_pages(k_cache, v_cache, src, dst, k_scale=None, v_scale=None, stream=None):
     """Page src[i] of the caches to page dst[i] (int32 [n], device), with its scales."""
     k_cache, v_cache, eb = _need_cache(k_cache, v_cache, k_scale, v_scale)
