@@ -1060,12 +1060,19 @@ def cache_compact(k_cache, v_cache, block_table, seq_lens, block_table_out, free
                                      _stream(stream)), "fa_cache_compact")
 
 
+def _on_device_of(stream):
+    return _same_device if stream is None else torch.cuda.device(stream.device)
+
+
 def selftest_watchdog(stream=None) -> int:
     """Launch the watchdog diagnostic (a wait that must time out); read the
     result with check_device_error()."""
-    return int(_lib.fa_selftest_watchdog(_stream(stream)))
+    with _on_device_of(stream):
+        return int(_lib.fa_selftest_watchdog(_stream(stream)))
 
 
 def check_device_error(stream=None) -> int:
-    """Synchronise the stream and return (and clear) the device error status."""
-    return int(_lib.fa_check_device_error(_stream(stream)))
+    """Synchronise the stream and return (and clear) the device error status of
+    its device (of the current one without a stream)."""
+    with _on_device_of(stream):
+        return int(_lib.fa_check_device_error(_stream(stream)))

@@ -612,8 +612,9 @@ const char *fa_status_string(int status);
 /*
  * Synchronises `stream`, then reads and clears the device error word that a
  * kernel sets when one of its bounded waits runs out, it meets an input it
- * cannot honour, or a cache call finds no free page.  Returns FA_OK,
- * FA_ERR_TIMEOUT, FA_ERR_INVALID_ARG, FA_ERR_PAGES or FA_ERR_CUDA.
+ * cannot honour, or a cache call finds no free page.  Each device has its own
+ * word; the current device's is read.  Returns FA_OK, FA_ERR_TIMEOUT,
+ * FA_ERR_INVALID_ARG, FA_ERR_PAGES or FA_ERR_CUDA.
  */
 int fa_check_device_error(void *stream);
 

@@ -65,3 +65,23 @@ def test_the_call_runs_inside_the_stream(fa, name, monkeypatch):
     with pytest.raises(Exception):          # (no GPU, and arguments of one shape for all)
         getattr(fa, name)(*arguments(fa, name), stream=st)
     assert seen and all(s == [st] for s in seen)
+
+
+@pytest.mark.parametrize("name", ["check_device_error", "selftest_watchdog"])
+def test_the_error_word_is_the_streams_devices(fa, name, monkeypatch):
+    """Each device has its own error word: the one of the stream's device is read, whichever device is current."""
+    inside, seen = [], []
+
+    @contextlib.contextmanager
+    def enter(device):
+        inside.append(device)
+        yield
+        inside.pop()
+
+    class Library:
+        def __getattr__(self, _):
+            return lambda *a: seen.append(list(inside)) or 0
+    monkeypatch.setattr(torch.cuda, "device", enter)
+    monkeypatch.setattr(fa, "_lib", Library())
+    assert getattr(fa, name)(stream=Stream(1)) == 0
+    assert seen == [[torch.device("cuda", 1)]]
