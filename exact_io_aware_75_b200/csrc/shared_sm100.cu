@@ -42,7 +42,6 @@
 //     half of a block's keys (P = 0 in the other's), and four warps share the
 //     exponentials instead of two.
 //   * shared_combine_kernel joins the partials of each row.
-#include <atomic>
 #include <climits>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -1429,17 +1428,10 @@ int launch(const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, const 
     using C = Cfg<D>;
     constexpr int smem = C::kOffTable + (int)sizeof(Table) + 1024;
     static_assert(smem + sizeof(Shared) <= 232448, "shared memory");
-    // once per device: the attribute stays
-    static std::atomic<uint64_t> ready{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return -5;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(shared_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 smem) != cudaSuccess)
-            return -5;
-        ready.fetch_or(bit, std::memory_order_relaxed);
-    }
+    // (on every call: the attribute goes with the device's context)
+    if (cudaFuncSetAttribute(shared_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess)
+        return -5;
     shared_kernel<D, PAGED><<<p.n * p.Hkv, kThreads, smem, stream>>>(tk, tv, p);
     if (cudaGetLastError() != cudaSuccess) return -5;
     // The combine is set up while the main kernel's last CTAs run.
