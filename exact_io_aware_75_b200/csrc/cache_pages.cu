@@ -225,31 +225,60 @@ append_kernel(Pages pg, const uint4 *__restrict__ k_new, const uint4 *__restrict
         len = __ldg(lens + s);
         return a >= 0 && n >= 0 && a <= total - n && len >= 0 && len <= max_pages * kPage - n;
     };
-    int running = 0, left = INT_MAX;
-    for (int s0 = 0; s0 < num_seqs; s0 += kThreads) {
-        const int s = s0 + tid;
-        int len = 0, n = 0, need = 0;
-        bool ok = false;
-        if (s < num_seqs) {
-            ok = ask(s, len, n);
-            if (ok) need = pages_of(len + n) - pages_of(len);
-            else if (blockIdx.x == 0) report_error(kDevErrInput);
-        }
-        int sum;
-        const int base = running + block_scan(need, s_warp, sum);
-        running += sum;
-        if (s < num_seqs) {
-            if (ok && need > 0 && base > count - need) {      // out of pages
-                left = min(left, base);
-                ok = false;
-                if (blockIdx.x == 0) report_error(kDevErrPages);
+    int running, left;
+    // marked: s_base holds -1 for sequences that are left out already; true if an
+    // offset descends or leaves [0, total]
+    auto plan = [&](bool marked) -> bool {
+        bool bad = false;
+        running = 0;
+        left = INT_MAX;
+        for (int s0 = 0; s0 < num_seqs; s0 += kThreads) {
+            const int s = s0 + tid;
+            int len = 0, n = 0, need = 0;
+            bool ok = false;
+            if (s < num_seqs) {
+                ok = ask(s, len, n) && !(marked && s_base[s] < 0);
+                if (ok) {
+                    need = pages_of(len + n) - pages_of(len);
+                } else {
+                    const int a = __ldg(cu + s);
+                    bad |= a < 0 || n < 0 || a > total - n;
+                    if (blockIdx.x == 0) report_error(kDevErrInput);
+                }
             }
-            s_base[s] = ok ? base : -1;
+            int sum;
+            const int base = running + block_scan(need, s_warp, sum);
+            running += sum;
+            if (s < num_seqs) {
+                if (ok && need > 0 && base > count - need) {      // out of pages
+                    left = min(left, base);
+                    ok = false;
+                }
+                s_base[s] = ok ? base : -1;
+            }
         }
+        return bad;
+    };
+    const bool unsorted = __syncthreads_or(plan(false));
+    if (unsorted) {
+        // the sequences whose tokens lie behind those of the ones before are
+        // appended to, the others are left out
+        if (tid == 0) {
+            int end = 0;
+            for (int s = 0; s < num_seqs; ++s) {
+                const int a = __ldg(cu + s), e = __ldg(cu + s + 1);
+                const bool good = a >= end && e >= a && e <= total;
+                s_base[s] = good ? 0 : -1;
+                if (good) end = e;
+            }
+        }
+        __syncthreads();
+        plan(true);
+        __syncthreads();
     }
+    if (left != INT_MAX && blockIdx.x == 0) report_error(kDevErrPages);
     // pages handed out: all, or those before the first sequence left out
     left = __reduce_min_sync(0xffffffffu, left);
-    __syncthreads();
     if (lane_id() == 0) s_warp[warp_id()] = left;
     __syncthreads();
     if (blockIdx.x == 0 && tid == 0) {
@@ -272,7 +301,10 @@ append_kernel(Pages pg, const uint4 *__restrict__ k_new, const uint4 *__restrict
     for (int i = tid; i < nt; i += kThreads) {
         const int t = t0 + i;
         int lo = 0, hi = num_seqs;          // the last s with cu[s] <= t
-        while (hi - lo > 1) {
+        if (unsorted)                       // (of those not left out)
+            for (int s = 0; s < num_seqs; ++s)
+                if (s_base[s] >= 0 && __ldg(cu + s) <= t) lo = s;
+        while (!unsorted && hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
         }

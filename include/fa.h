@@ -558,7 +558,9 @@ int fa_decode_paged_noalloc(const void *q, const void *k_cache, const void *v_ca
  *   seq_lens_out [num_seqs], free_count_out [1]: written; must not be
  *   seq_lens, free_count (FA_ERR_INVALID_ARG).  A slot for which the free
  *   pages do not suffice, or that would not fit its row, is left as it was
- *   (its length copied); slots behind it that need no page go on.  A partly
+ *   (its length copied); slots behind it that need no page go on.  So is a
+ *   slot whose tokens do not lie within k_new behind those of the slots before
+ *   it that are appended to.  A partly
  *   filled last page must belong to its slot alone (fa_cache_fork sees to
  *   that).  At most 8192 slots.
  *
