@@ -40,6 +40,9 @@ struct Pages {
     int tok16;             // 16-byte words per token (K or V)
 };
 
+__device__ __forceinline__ bool exists(const Pages &pg, int page) {
+    return page >= 0 && page < pg.num_pages;
+}
 __device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
 
 // Sum of one value per thread; every thread gets the block's total.
@@ -176,7 +179,7 @@ fork_kernel(Pages pg, const int *__restrict__ table, const int *__restrict__ len
         if (copies(i)) {
             const int r = rank++;
             if (r < count) fresh = __ldg(free_pages + count - 1 - r);
-            if (r >= count || fresh < 0 || fresh >= pg.num_pages) {
+            if (r >= count || !exists(pg, fresh)) {
                 report_error(r >= count ? kDevErrPages : kDevErrInput);
                 fresh = -1;
                 len = 0;                   // the slot stays empty
@@ -185,16 +188,20 @@ fork_kernel(Pages pg, const int *__restrict__ table, const int *__restrict__ len
         const int used = pages_of(len);
         const int *row = table + (size_t)(p < 0 ? 0 : p) * max_pages;
         if (blockIdx.y == 0) {
-            for (int c = tid; c < used; c += kThreads) {
-                const int page = __ldg(row + c);
-                if (page < 0 || page >= pg.num_pages) report_error(kDevErrInput);
-                table_out[(size_t)i * max_pages + c] = (fresh >= 0 && c == used - 1) ? fresh : page;
+            // (so does one whose parent names a page that does not exist)
+            bool bad = false;
+            for (int c = tid; c < used; c += kThreads) bad |= !exists(pg, __ldg(row + c));
+            const bool keep = !__syncthreads_or(bad);
+            for (int c = tid; keep && c < used; c += kThreads)
+                table_out[(size_t)i * max_pages + c] = (fresh >= 0 && c == used - 1) ? fresh : __ldg(row + c);
+            if (tid == 0) {
+                lens_out[i] = keep ? len : 0;
+                if (!keep) report_error(kDevErrInput);
             }
-            if (tid == 0) lens_out[i] = len;
         }
         if (fresh >= 0) {
             const int src = __ldg(row + used - 1);
-            if (src >= 0 && src < pg.num_pages && src != fresh)
+            if (exists(pg, src) && src != fresh)
                 copy_page(pg, src, fresh, rest, blockIdx.y == 0, blockIdx.y == 1);
         }
     }
@@ -290,11 +297,20 @@ append_kernel(Pages pg, const uint4 *__restrict__ k_new, const uint4 *__restrict
         int len, n;
         ask(s, len, n);
         const int base = s_base[s];
-        if (tid == 0) lens_out[s] = base >= 0 ? len + n : len;
-        if (base < 0) continue;
-        const int used = pages_of(len), used_new = pages_of(len + n);
-        for (int c = used + tid; c < used_new; c += kThreads)
-            table[(size_t)s * max_pages + c] = __ldg(free_pages + count - 1 - (base + c - used));
+        bool add = base >= 0;
+        if (add && n > 0) {
+            // the pages its tokens go to must exist, or it is left out
+            const int used = pages_of(len), used_new = pages_of(len + n);
+            const int *page = free_pages + count - 1 - base + used;
+            bool bad = false;
+            if (tid == 0 && len % kPage) bad = !exists(pg, __ldcg(table + (size_t)s * max_pages + used - 1));
+            for (int c = used + tid; c < used_new; c += kThreads) bad |= !exists(pg, __ldg(page - c));
+            add = !__syncthreads_or(bad);
+            for (int c = used + tid; add && c < used_new; c += kThreads)
+                table[(size_t)s * max_pages + c] = __ldg(page - c);
+            if (!add && tid == 0) report_error(kDevErrInput);
+        }
+        if (tid == 0) lens_out[s] = add ? len + n : len;
     }
     const int t0 = blockIdx.x * per_block, nt = min(per_block, total - t0);
     if (nt <= 0) return;
@@ -314,7 +330,7 @@ append_kernel(Pages pg, const uint4 *__restrict__ k_new, const uint4 *__restrict
             // (entries below `used` are not written by this launch)
             const int page = c < used ? __ldcg(table + (size_t)lo * max_pages + c)
                                       : __ldg(free_pages + count - 1 - (s_base[lo] + c - used));
-            if (page >= 0 && page < pg.num_pages) row = page * kPage + pos % kPage;
+            if (exists(pg, page)) row = page * kPage + pos % kPage;
             else report_error(kDevErrInput);
         }
         s_row[i] = row;

@@ -546,8 +546,9 @@ int fa_decode_paged_noalloc(const void *q, const void *k_cache, const void *v_ca
  *   block_table_out [num_new, max_pages_per_seq], seq_lens_out [num_new],
  *   free_count_out [1]: written; must not overlap block_table, seq_lens,
  *   free_count (FA_ERR_INVALID_ARG).  Entries past a row's used ones are left
- *   as they were.  A slot without a free page, or with a parent out of range,
- *   comes out empty.  At most 8192 slots (FA_ERR_UNSUPPORTED).
+ *   as they were.  A slot without a free page, with a parent out of range, or
+ *   whose parent names a page that does not exist, comes out empty.  At most
+ *   8192 slots (FA_ERR_UNSUPPORTED).
  *
  * fa_cache_append: new tokens behind the sequences' ends (bf16 caches).
  *   k_new, v_new [total_new, Hkv, d] bf16, packed by cu_new [num_seqs + 1]
@@ -560,9 +561,10 @@ int fa_decode_paged_noalloc(const void *q, const void *k_cache, const void *v_ca
  *   pages do not suffice, or that would not fit its row, is left as it was
  *   (its length copied); slots behind it that need no page go on.  So is a
  *   slot whose tokens do not lie within k_new behind those of the slots before
- *   it that are appended to.  A partly
- *   filled last page must belong to its slot alone (fa_cache_fork sees to
- *   that).  At most 8192 slots.
+ *   it that are appended to, and one that would get a page that does not exist
+ *   or has such a partly filled last page (places behind its end, and the pages
+ *   taken for it, may have been written).  A partly filled last page must
+ *   belong to its slot alone (fa_cache_fork sees to that).  At most 8192 slots.
  *
  * fa_cache_collect: free_pages and free_count from the tables: every page
  * not in use, in descending order, so that the lowest is handed out first.
