@@ -972,16 +972,22 @@ bwd_convert_kernel(const float *__restrict__ acc, uint16_t *__restrict__ dq, lon
     reinterpret_cast<uint4 *>(dq)[i] = o;
 }
 
-// Zeros into rows cu[0] .. cu[num_seqs]-1 of two tensors (all rows without
-// cu); n8 16-byte words, per8 per row.  Cross attention without any query.
+// Cross attention without any query: zeros into the sequences' rows of dK and
+// dV; per8 16-byte words per row.
 __global__ void __launch_bounds__(256)
-bwd_zero_kernel(uint4 *__restrict__ dk, uint4 *__restrict__ dv, long long n8,
-                const int *__restrict__ cu, int num_seqs, int per8) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n8) return;
-    if (cu && (i / per8 < __ldg(cu) || i / per8 >= __ldg(cu + num_seqs))) return;
-    dk[i] = make_uint4(0u, 0u, 0u, 0u);
-    dv[i] = make_uint4(0u, 0u, 0u, 0u);
+bwd_zero_kernel(uint4 *__restrict__ dk, uint4 *__restrict__ dv, const Params p, int per8) {
+    for (int s = 0; s < p.num_seqs; ++s) {
+        int tok0, L, tokk0, Lk, Ls;
+        if (!cross_lengths(p, s, tok0, L, tokk0, Lk, Ls)) {
+            if (blockIdx.x == 0 && threadIdx.x == 0) report_error(kDevErrInput);
+            continue;
+        }
+        const long long first = (long long)tokk0 * per8, n = (long long)Ls * per8;
+        for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += 256ll * gridDim.x) {
+            dk[first + i] = make_uint4(0u, 0u, 0u, 0u);
+            dv[first + i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
 }
 
 }  // namespace bwd_impl
@@ -999,13 +1005,31 @@ int launch_bwd(const BwdArgs &a, cudaStream_t stream) {
     const int dh = a.d;
     const long long total = a.total_tokens;
     if (a.num_seqs == 0) return 0;
+    Params p{};
+    p.lse = a.lse;
+    p.dk = a.dk;
+    p.dv = a.dv;
+    p.cu_seqlens = a.cu_seqlens;
+    p.num_seqs = a.num_seqs;
+    p.seqlen = a.seqlen;
+    p.total_tokens = (int)total;
+    p.max_seqlen = a.max_seqlen;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.group = a.Hq / a.Hkv;
+    p.causal = a.causal;
+    p.window = a.causal ? a.window : 0;
+    p.scale = a.scale;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.cu_seqlens_k = a.cu_seqlens_k;
+    p.seq_lens_k = a.seq_lens_k;
+    p.seqlen_k = a.seqlen_k;
+    p.total_k = a.total_k;
+    p.max_seqlen_k = a.max_seqlen_k;
     if (total == 0) {
         if (!a.cross || a.total_k == 0) return 0;
-        const int per8 = a.Hkv * dh / 8;
-        const long long n8 = (long long)a.total_k * per8;
-        bwd_zero_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, stream>>>(
-            static_cast<uint4 *>(a.dk), static_cast<uint4 *>(a.dv), n8, a.cu_seqlens_k, a.num_seqs,
-            per8);
+        bwd_zero_kernel<<<4 * device_sm_count(), 256, 0, stream>>>(
+            static_cast<uint4 *>(a.dk), static_cast<uint4 *>(a.dv), p, a.Hkv * dh / 8);
         return cudaGetLastError() == cudaSuccess ? 0 : -5;
     }
     const size_t acc_bytes = ((size_t)total * a.Hq * dh * sizeof(float) + 255) & ~(size_t)255;
@@ -1043,30 +1067,11 @@ int launch_bwd(const BwdArgs &a, cudaStream_t stream) {
         encode_tensor_map_3d(&tdq, dq_acc, 4, dh, a.Hq, T, (uint64_t)dh * 4,
                              (uint64_t)a.Hq * dh * 4, dh, 1, kDQHalf, 0))
         return -5;
-    Params p;
-    p.lse = a.lse;
     p.dd = dd;
     p.dq_acc = dq_acc;
-    p.dk = a.dk;
-    p.dv = a.dv;
-    p.cu_seqlens = a.cu_seqlens;
-    p.num_seqs = a.num_seqs;
-    p.seqlen = a.seqlen;
-    p.total_tokens = (int)total;
-    p.max_seqlen = a.max_seqlen;
-    p.Hq = a.Hq;
-    p.Hkv = a.Hkv;
-    p.group = a.Hq / a.Hkv;
-    p.causal = a.causal;
-    p.window = a.causal ? a.window : 0;
-    p.scale = a.scale;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
-    p.cu_seqlens_k = a.cu_seqlens_k;
-    p.seq_lens_k = a.seq_lens_k;
-    p.seqlen_k = a.seqlen_k;
-    p.total_k = a.total_k;
-    p.max_seqlen_k = a.max_seqlen_k;
+    // (cross attention: a unit at least per sequence, which finds lengths above the longest)
     p.num_kblocks = ((a.cross ? a.max_seqlen_k : a.max_seqlen) + kBlockK - 1) / kBlockK;
+    if (a.cross && a.total_k > 0 && p.num_kblocks == 0) p.num_kblocks = 1;
     const long long units = (long long)p.num_kblocks * a.num_seqs * a.Hkv;
     if (units > (1ll << 30)) return -2;
     p.num_units = (int)units;

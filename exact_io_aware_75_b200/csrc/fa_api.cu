@@ -800,7 +800,7 @@ int fwd_cross_call(const void *q, const void *k, const void *v, void *o, float *
         return FA_ERR_INVALID_ARG;
     int rc = check_common(Hq, Hkv, d, 0, 0, scale, o_dtype);
     if (rc) return rc;
-    if (num_seqs == 0 || total_q == 0 || max_q == 0) return FA_OK;
+    if (num_seqs == 0 || total_q == 0) return FA_OK;
     rc = check_cross(q, k, v, o, lse, seq_lens_k, cu_q, cu_k, packed, total_q, total_k);
     if (rc) return rc;
     fa::PrefillArgs a{};

@@ -1164,7 +1164,8 @@ Params make_params(const PrefillArgs &a) {
     p.max_seqlen_k = a.max_seqlen_k;
     p.pack = p.group <= kBlockM ? p.group : 1;
     p.tile_tok = kBlockM / p.pack;
-    if (a.cross) p.num_mblocks = (a.max_seqlen + 2 * p.tile_tok - 1) / (2 * p.tile_tok);
+    // (a unit at least per sequence, which finds lengths above the longest)
+    if (a.cross) p.num_mblocks = a.max_seqlen > 0 ? (a.max_seqlen + 2 * p.tile_tok - 1) / (2 * p.tile_tok) : 1;
     return p;
 }
 
