@@ -598,7 +598,7 @@ def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, ou
         scale = 1.0 / math.sqrt(d)
     out, lse, od = _out_pair(out, lse, (B, Nq, Hq, d), (B, Hq, Nq), out_dtype, return_lse, q)
     if split_keys is None:
-        split_keys = (od == FA_OUT_BF16 and 0 < Hkv and Hq % Hkv == 0 and Nk < 1 << 22
+        split_keys = (od == FA_OUT_BF16 and 0 < Hkv <= Hq and Hq % Hkv == 0 and Nk < 1 << 22
                       and _split_is_faster(B, Nq, Nk, Hq, Hkv, d, _sm_count(q.get_device()))
                       and decode_cross_workspace_bytes(B, Hq, Hkv, Nq, d) > 0)
     if split_keys:
