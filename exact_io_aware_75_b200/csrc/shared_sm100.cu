@@ -74,9 +74,11 @@ constexpr int kFewRows = 32;                // rows at most in the transposed fo
 constexpr int kSBufs = 4;                   // S^T buffers per warpgroup, 32 columns each
 // What a key block costs a CTA, by the item's rows, and an item besides (its
 // first loads and its epilogue).  Measured on prefixes of 131,072 tokens, 8 KV
-// heads, us per block: d = 128 1.31 (4 rows), 1.34 (128), 2.18 (256); d = 64
-// 0.80 (4), 0.76 (16), 1.00 (32), 1.17 (128), 2.18 (256).  Up to 128 rows at
-// d = 128 that is the rate of HBM, 7.0 to 7.2 TB/s.
+// heads, us per block: d = 128 1.32 (4 rows), 1.35 (32), 1.33 to 1.41 (36 to
+// 128), 2.09 (132), 2.16 (192), 2.27 (256); d = 64 0.81 (4), 0.86 (16), 1.02
+// (32), 0.99 (36), 1.11 (64), 1.17 to 1.24 (68 to 96), 1.47 (128), 2.33 (132),
+// 2.37 (192), 2.64 (256).  Up to 128 rows at d = 128 that is the rate of HBM,
+// 6.7 to 7.2 TB/s.
 template <int D>
 struct Cost {
     static constexpr int kFew = 3, kOne = D == 128 ? 3 : 4, kPair = D == 128 ? 5 : 8;
@@ -1297,10 +1299,13 @@ shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 
 // ---------------------------------------------------------------- combine
 // The partials of one (token, query head) row, by SPLIT of a block's eight
-// warps: eight where there are few rows and so many partials each, else one
-// (32 rows of 18 partials: 11 us after the main kernel with one, FIXME with eight).
+// warps: eight where there are few rows and so many partials each, else one.
+// Whole calls, 32/8 heads, d = 128, us with eight and one: 32 rows of 32,768
+// tokens 33.9 and 37.4, 256 of 4,096 33.4 and 33.8, 384 of 2,048 24.5 and 24.7,
+// 448 of 2,048 31.1 and 31.0, 512 34.2 and 33.7 (16/16 heads, d = 64: 54.7 and
+// 55.5), 1,024 of 512 21.4 and 19.7, 2,048 of 512 40.1 and 34.6.
 constexpr int kCombineWarps = 8;
-constexpr int kCombineFewRows = 1024;
+constexpr int kCombineFewRows = 448;
 
 template <int D, bool PAGED, int SPLIT>
 __global__ void __launch_bounds__(32 * kCombineWarps)

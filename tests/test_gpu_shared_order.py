@@ -33,3 +33,12 @@ def test_many_rows_and_few_in_turn(fa, Hq, Hkv, d, seed):
         o, lse = b.run(fa)
         assert fa.check_device_error() == 0
     b.check(o, lse)
+
+
+@pytest.mark.parametrize("S", [1, 55, 56, 57, 128, 129])
+def test_rows_at_the_borders_of_the_combine(fa, S):
+    """440 to 456 rows, and few and many: joined by a block's eight warps or by one."""
+    b = Batch([700 + 3 * (i % 50) for i in range(S)], [(0, S)] if S > 1 else [], [300] if S > 1 else [], 8, 2, 64, seed=S)
+    o, lse = b.run(fa)
+    assert fa.check_device_error() == 0
+    b.check(o, lse)
