@@ -30,7 +30,6 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
-import inspect
 import math
 import os
 
@@ -196,30 +195,20 @@ def _stream(stream=None):
     return torch.cuda.current_stream().cuda_stream
 
 
-def _on_stream(f):
+def _inside(f, stream, args):
     """f(..., stream=s) as f(...) inside torch.cuda.stream(s), so that what f allocates (its
     workspace, outputs not passed) belongs to s: in the pool of the caller's stream a
-    workspace could be handed out again while the kernels on s still use it."""
-    names = list(inspect.signature(f).parameters)
-    first, at = names[0], names.index("stream")
-
-    @functools.wraps(f)
-    def call(*args, **kwargs):
-        stream = args[at] if len(args) > at else kwargs.get("stream")
-        if stream is None:
-            return f(*args, **kwargs)
-        x = args[0] if args else kwargs.get(first)
-        if isinstance(x, dict):                  # fp8_prepare's operands
-            x = next(iter(x.values()), None)
-        if isinstance(x, torch.Tensor) and x.is_cuda and x.device != stream.device:
-            raise FAError(FA_ERR_INVALID_ARG, f"a stream of {stream.device}, {first} on {x.device}")
-        if len(args) > at:
-            args = args[:at] + (None,) + args[at + 1:]
-        else:
-            kwargs["stream"] = None
-        with torch.cuda.stream(stream):
-            return f(*args, **kwargs)
-    return call
+    workspace could be handed out again while the kernels on s still use it.  ``args``: f's
+    arguments by name.  (A line in each call instead of a decorator, which cost every call
+    without a stream 0.5 us.)"""
+    name, x = next(iter(args.items()))
+    if isinstance(x, dict):                  # fp8_prepare's operands
+        x = next(iter(x.values()), None)
+    if isinstance(x, torch.Tensor) and x.is_cuda and x.device != stream.device:
+        raise FAError(FA_ERR_INVALID_ARG, f"a stream of {stream.device}, {name} on {x.device}")
+    args["stream"] = None
+    with torch.cuda.stream(stream):
+        return f(**args)
 
 
 def _check(rc: int, where: str):
@@ -244,7 +233,6 @@ def _need(t, dtype, ndim, name):
         raise FAError(FA_ERR_INVALID_ARG, f"{name} must be contiguous")
 
 
-@_on_stream
 def fwd(q, k, v, causal=False, window=0, scale=None, out_dtype=torch.bfloat16,
         out=None, lse=None, return_lse=True, stream=None, sinks=None, doc_ids=None,
         sink_tokens=None):
@@ -252,6 +240,8 @@ def fwd(q, k, v, causal=False, window=0, scale=None, out_dtype=torch.bfloat16,
     ``sinks`` (fp32 [Hq], device) selects fa_fwd_sinks; ``doc_ids`` (int32 [B,N],
     device) selects fa_fwd_doc; ``sink_tokens`` (an int, with causal and a window)
     selects fa_fwd_sink_tokens."""
+    if stream is not None:
+        return _inside(fwd, stream, locals())
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, torch.bfloat16, 4, n)
     B, N, Hq, d = q.shape
@@ -300,13 +290,14 @@ def fp8_workspace_bytes(B, N, Hkv) -> int:
     return int(_lib.fa_fp8_workspace_bytes(int(B), int(N), int(Hkv)))
 
 
-@_on_stream
 def fp8_prepare(q, k, v, signs=None, out=None, workspace=None, stream=None):
     """E4M3 operands of the FP8 prefill.  q [B,N,Hq,128], k/v [B,N,Hkv,128] bf16;
     signs fp32 [128] of +-1 (device) or None (no rotation).  Returns a dict with
     q8 [B,N,Hq,128], k8 [B,N,Hkv,128] uint8 codes, vt8 [B,Hkv,128,vt_stride]
     uint8 (V transposed), q_scale [B,Hq,nblk], k_scale [B,Hkv,nblk], v_scale
     [B,Hkv] fp32.  ``out`` may be such a dict to fill in place."""
+    if stream is not None:
+        return _inside(fp8_prepare, stream, locals())
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, torch.bfloat16, 4, n)
     B, N, Hq, d = q.shape
@@ -338,10 +329,11 @@ def fp8_prepare(q, k, v, signs=None, out=None, workspace=None, stream=None):
     return out
 
 
-@_on_stream
 def fwd_fp8(prep, causal=False, window=0, scale=None, out_dtype=torch.bfloat16, out=None,
             lse=None, return_lse=True, stream=None):
     """FP8 prefill on fp8_prepare's operands -> (O [B,N,Hq,128], LSE [B,Hq,N])."""
+    if stream is not None:
+        return _inside(fwd_fp8, stream, locals())
     q8, k8, vt8 = prep["q8"], prep["k8"], prep["vt8"]
     _need(q8, torch.uint8, 4, "q8")
     _need(k8, torch.uint8, 4, "k8")
@@ -364,13 +356,14 @@ def fwd_fp8(prep, causal=False, window=0, scale=None, out_dtype=torch.bfloat16, 
     return out, lse
 
 
-@_on_stream
 def fwd_varlen(q, k, v, cu_seqlens, max_seqlen, causal=False, window=0, scale=None,
                out_dtype=torch.bfloat16, out=None, lse=None, return_lse=True, stream=None,
                sinks=None, sink_tokens=None):
     """Packed prefill.  q [T,Hq,d], k/v [T,Hkv,d], cu_seqlens [S+1] int32 (device)
     -> (O [T,Hq,d], LSE [Hq,T]).  ``sinks`` selects fa_fwd_varlen_sinks;
     ``sink_tokens`` (an int, with causal and a window) fa_fwd_varlen_sink_tokens."""
+    if stream is not None:
+        return _inside(fwd_varlen, stream, locals())
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, torch.bfloat16, 3, n)
     _need(cu_seqlens, torch.int32, 1, "cu_seqlens")
@@ -407,13 +400,14 @@ def fwd_varlen(q, k, v, cu_seqlens, max_seqlen, causal=False, window=0, scale=No
     return out, lse
 
 
-@_on_stream
 def fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k, max_seqlen_q,
               causal=True, window=0, scale=None, sinks=None, out_dtype=torch.bfloat16, out=None,
               lse=None, return_lse=True, stream=None):
     """Chunked prefill over a paged cache.  q [Tq,Hq,d] (each sequence's last L_q
     tokens), caches [P,16,Hkv,d], block_table [S,maxp], cu_seqlens_q [S+1],
     seq_lens_k [S] -> (O [Tq,Hq,d], LSE [Hq,Tq])."""
+    if stream is not None:
+        return _inside(fwd_paged, stream, locals())
     _need(q, torch.bfloat16, 3, "q")
     _need(k_cache, torch.bfloat16, 4, "k_cache")
     _need(v_cache, torch.bfloat16, 4, "v_cache")
@@ -443,12 +437,13 @@ def bwd_workspace_bytes(total_tokens, Hq, d) -> int:
     return int(_lib.fa_bwd_workspace_bytes(int(total_tokens), int(Hq), int(d)))
 
 
-@_on_stream
 def bwd(q, k, v, o, dout, lse, causal=False, window=0, scale=None, dq=None, dk=None, dv=None,
         workspace=None, stream=None, sinks=None, dsinks=None):
     """Dense backward.  q/o/dout [B,N,Hq,d], k/v [B,N,Hkv,d] bf16, lse [B,Hq,N] fp32
     (from fwd) -> (dQ, dK, dV) bf16; with ``sinks`` (the forward's sink logits,
     fp32 [Hq]) fa_bwd_sinks, returning (dQ, dK, dV, dsinks)."""
+    if stream is not None:
+        return _inside(bwd, stream, locals())
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (dout, "dout")):
         _need(t, torch.bfloat16, 4, n)
     _need(lse, torch.float32, 3, "lse")
@@ -483,11 +478,12 @@ def bwd(q, k, v, o, dout, lse, causal=False, window=0, scale=None, dq=None, dk=N
     return dq, dk, dv
 
 
-@_on_stream
 def bwd_varlen(q, k, v, o, dout, lse, cu_seqlens, max_seqlen, causal=False, window=0,
                scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Packed backward.  q/o/dout [T,Hq,d], k/v [T,Hkv,d], lse [Hq,T], cu_seqlens [S+1]
     -> (dQ, dK, dV) bf16."""
+    if stream is not None:
+        return _inside(bwd_varlen, stream, locals())
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (dout, "dout")):
         _need(t, torch.bfloat16, 3, n)
     _need(lse, torch.float32, 2, "lse")
@@ -582,13 +578,14 @@ def _cross_shapes(q, k, v, ndim):
         raise FAError(FA_ERR_INVALID_ARG, "q/k/v shape")
 
 
-@_on_stream
 def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, out=None, lse=None,
               return_lse=True, stream=None, split_keys=None):
     """Cross attention, dense.  q [B,Nq,Hq,d], k/v [B,Nk,Hkv,d] bf16, seq_lens_k [B] int32
     (device) or None -> (O [B,Nq,Hq,d], LSE [B,Hq,Nq]).  split_keys: through
     decode_cross (bf16 O only), or not; by default where the queries are few, as include/fa.h
     says there."""
+    if stream is not None:
+        return _inside(fwd_cross, stream, locals())
     _cross_shapes(q, k, v, 4)
     B, Nq, Hq, d = q.shape
     Nk, Hkv = k.shape[1:3]
@@ -610,11 +607,12 @@ def fwd_cross(q, k, v, seq_lens_k=None, scale=None, out_dtype=torch.bfloat16, ou
     return out, lse
 
 
-@_on_stream
 def fwd_varlen_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale=None,
                      out_dtype=torch.bfloat16, out=None, lse=None, return_lse=True, stream=None):
     """Cross attention, packed.  q [Tq,Hq,d], k/v [Tk,Hkv,d] bf16, cu_seqlens_q and
     cu_seqlens_k [S+1] int32 (device) -> (O [Tq,Hq,d], LSE [Hq,Tq])."""
+    if stream is not None:
+        return _inside(fwd_varlen_cross, stream, locals())
     _cross_shapes(q, k, v, 3)
     Tq, Hq, d = q.shape
     Tk, Hkv = k.shape[:2]
@@ -633,11 +631,12 @@ def fwd_varlen_cross(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
     return out, lse
 
 
-@_on_stream
 def bwd_cross(q, k, v, o, dout, lse, seq_lens_k=None, scale=None, dq=None, dk=None, dv=None,
               workspace=None, stream=None):
     """Backward of fwd_cross.  q/o/dout [B,Nq,Hq,d], k/v [B,Nk,Hkv,d] bf16, lse [B,Hq,Nq]
     -> (dQ, dK, dV) bf16."""
+    if stream is not None:
+        return _inside(bwd_cross, stream, locals())
     _cross_shapes(q, k, v, 4)
     B, Nq, Hq, d = q.shape
     Nk, Hkv = k.shape[1:3]
@@ -662,11 +661,12 @@ def bwd_cross(q, k, v, o, dout, lse, seq_lens_k=None, scale=None, dq=None, dk=No
     return dq, dk, dv
 
 
-@_on_stream
 def bwd_varlen_cross(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                      scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Backward of fwd_varlen_cross.  q/o/dout [Tq,Hq,d], k/v [Tk,Hkv,d] bf16, lse [Hq,Tq]
     -> (dQ, dK, dV) bf16."""
+    if stream is not None:
+        return _inside(bwd_varlen_cross, stream, locals())
     _cross_shapes(q, k, v, 3)
     Tq, Hq, d = q.shape
     Tk, Hkv = k.shape[:2]
@@ -697,13 +697,14 @@ def decode_shared_workspace_bytes(num_seqs, Hq, Hkv, d) -> int:
     return int(_lib.fa_decode_shared_workspace_bytes(int(num_seqs), int(Hq), int(Hkv), int(d)))
 
 
-@_on_stream
 def decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, scale=None,
                   sinks=None, out=None, lse=None, return_lse=True, workspace=None, stream=None):
     """Paged decode of sequences that share prefixes.  q [S,Hq,d], caches [P,16,Hkv,d],
     block_table [S,maxp], seq_lens [S], cu_groups [G+1], prefix_lens [G] int32: the sequences
     of group g name the same pages for their first prefix_lens[g] // 16 table entries
     -> (O [S,Hq,d] bf16, LSE [S,Hq])."""
+    if stream is not None:
+        return _inside(decode_shared, stream, locals())
     _need(q, torch.bfloat16, 3, "q")
     _need(k_cache, torch.bfloat16, 4, "k_cache")
     _need(v_cache, torch.bfloat16, 4, "v_cache")
@@ -741,12 +742,13 @@ def decode_cross_workspace_bytes(B, Hq, Hkv, Nq, d) -> int:
     return int(_lib.fa_decode_cross_workspace_bytes(int(B), int(Hq), int(Hkv), int(Nq), int(d)))
 
 
-@_on_stream
 def decode_cross(q, k, v, seq_lens_k=None, scale=None, out=None, lse=None, return_lse=True,
                  workspace=None, stream=None):
     """Cross attention of few queries, the keys split over the GPU.  q [B,Nq,Hq,d], k/v
     [B,Nk,Hkv,d] bf16, seq_lens_k [B] int32 (device) or None -> (O [B,Nq,Hq,d] bf16,
     LSE [B,Hq,Nq])."""
+    if stream is not None:
+        return _inside(decode_cross, stream, locals())
     _cross_shapes(q, k, v, 4)
     B, Nq, Hq, d = q.shape
     Nk, Hkv = k.shape[1:3]
@@ -769,11 +771,12 @@ def decode_workspace_bytes(num_seqs, Hq, d, page_size, max_pages_per_seq) -> int
                                               int(max_pages_per_seq)))
 
 
-@_on_stream
 def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None, lse=None,
                  return_lse=True, workspace=None, stream=None, sinks=None):
     """Paged decode.  q [S,Hq,d], caches [P,ps,Hkv,d], block_table [S,maxp] int32,
     seq_lens [S] int32 -> (O [S,Hq,d] bf16, LSE [S,Hq])."""
+    if stream is not None:
+        return _inside(decode_paged, stream, locals())
     _need(q, torch.bfloat16, 3, "q")
     _need(k_cache, torch.bfloat16, 4, "k_cache")
     _need(v_cache, torch.bfloat16, 4, "v_cache")
@@ -808,12 +811,13 @@ def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=Non
     return out, lse
 
 
-@_on_stream
 def decode_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, scale=None,
                      sinks=None, out=None, lse=None, return_lse=True, workspace=None,
                      stream=None):
     """Paged decode over an FP8 E4M3 cache.  k_codes/v_codes [P,ps,Hkv,d] uint8 (or
     float8_e4m3fn), k_scale/v_scale [P,Hkv] fp32 -> (O [S,Hq,d] bf16, LSE [S,Hq])."""
+    if stream is not None:
+        return _inside(decode_paged_fp8, stream, locals())
     _need(q, torch.bfloat16, 3, "q")
     if k_codes.dtype == torch.float8_e4m3fn:
         k_codes, v_codes = k_codes.view(torch.uint8), v_codes.view(torch.uint8)
@@ -846,13 +850,14 @@ def decode_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
     return out, lse
 
 
-@_on_stream
 def decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None,
                          lse=None, return_lse=True, stream=None):
     """Paged decode with the library's fixed device scratch instead of a
     workspace, for callers that cannot allocate device memory (see
     fa_decode_paged_noalloc in include/fa.h: 32 MiB limit, first call per
     device before any stream capture, overlapping calls race)."""
+    if stream is not None:
+        return _inside(decode_paged_noalloc, stream, locals())
     _need(q, torch.bfloat16, 3, "q")
     _need(k_cache, torch.bfloat16, 4, "k_cache")
     _need(v_cache, torch.bfloat16, 4, "v_cache")
@@ -926,7 +931,6 @@ def _bytes_of(workspace, need, like):
     return workspace
 
 
-@_on_stream
 def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, free_count,
                block_table_out, seq_lens_out, free_count_out, k_scale=None, v_scale=None,
                stream=None):
@@ -935,6 +939,8 @@ def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, fre
     caches [P,16,Hkv,d] (bf16, or E4M3 with scales [P,Hkv]), block_table [S,maxp], seq_lens
     [S], parents [N], free_pages [F], free_count [1] int32 -> writes block_table_out [N,maxp],
     seq_lens_out [N], free_count_out [1], which must not overlap the inputs."""
+    if stream is not None:
+        return _inside(cache_fork, stream, locals())
     k_cache, v_cache, eb = _need_cache(k_cache, v_cache, k_scale, v_scale)
     P, ps, Hkv, d = k_cache.shape
     _need(block_table, torch.int32, 2, "block_table")
@@ -959,13 +965,14 @@ def cache_fork(k_cache, v_cache, block_table, seq_lens, parents, free_pages, fre
                                   _stream(stream)), "fa_cache_fork")
 
 
-@_on_stream
 def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, free_pages,
                  free_count, seq_lens_out, free_count_out, stream=None):
     """New tokens behind the sequences' ends.  k_new, v_new [T,Hkv,d] bf16 packed by cu_new
     [S+1]; caches [P,16,Hkv,d] bf16; block_table [S,maxp] (gets the pages taken), seq_lens
     [S], free_pages [F], free_count [1] int32 -> writes seq_lens_out [S], free_count_out [1],
     which must not be the inputs."""
+    if stream is not None:
+        return _inside(cache_append, stream, locals())
     _need(k_new, torch.bfloat16, 3, "k_new")
     _need(v_new, torch.bfloat16, 3, "v_new")
     _need(k_cache, torch.bfloat16, 4, "k_cache")
@@ -993,9 +1000,10 @@ def cache_append(k_new, v_new, cu_new, k_cache, v_cache, block_table, seq_lens, 
                "fa_cache_append")
 
 
-@_on_stream
 def cache_copy_pages(k_cache, v_cache, src, dst, k_scale=None, v_scale=None, stream=None):
     """Page src[i] of the caches to page dst[i] (int32 [n], device), with its scales."""
+    if stream is not None:
+        return _inside(cache_copy_pages, stream, locals())
     k_cache, v_cache, eb = _need_cache(k_cache, v_cache, k_scale, v_scale)
     P, ps, Hkv, d = k_cache.shape
     _need(src, torch.int32, 1, "src")
@@ -1010,11 +1018,12 @@ def cache_collect_workspace_bytes(num_pages) -> int:
     return int(_lib.fa_cache_collect_workspace_bytes(int(num_pages)))
 
 
-@_on_stream
 def cache_collect(block_table, seq_lens, free_pages, free_count, page_size=16, workspace=None,
                   stream=None):
     """The pages that no sequence uses, descending, into free_pages [P] and free_count [1]
     (int32, device), from block_table [S,maxp] and seq_lens [S]."""
+    if stream is not None:
+        return _inside(cache_collect, stream, locals())
     _need(block_table, torch.int32, 2, "block_table")
     _need(free_pages, torch.int32, 1, "free_pages")
     S, maxp = block_table.shape
@@ -1034,12 +1043,13 @@ def cache_compact_workspace_bytes(num_pages) -> int:
     return int(_lib.fa_cache_compact_workspace_bytes(int(num_pages)))
 
 
-@_on_stream
 def cache_compact(k_cache, v_cache, block_table, seq_lens, block_table_out, free_pages, free_count,
                   k_scale=None, v_scale=None, workspace=None, stream=None):
     """Moves the pages in use to the cache's front.  caches [P,16,Hkv,d] (bf16, or E4M3 with
     scales), block_table [S,maxp], seq_lens [S] int32 -> writes block_table_out [S,maxp] (may
     be block_table), free_pages [P], free_count [1]."""
+    if stream is not None:
+        return _inside(cache_compact, stream, locals())
     k_cache, v_cache, eb = _need_cache(k_cache, v_cache, k_scale, v_scale)
     P, ps, Hkv, d = k_cache.shape
     _need(block_table, torch.int32, 2, "block_table")

@@ -7,8 +7,10 @@
 // row cost nearly the same, and CTAs at work at the same time share a sequence
 // and its keys.  (Equal contiguous parts of the units, the other way, were 11 %
 // slower on equal lengths.)  Each CTA orders the sequences for itself.  More
-// than kDealSeqs of them are dealt as they come: there are many units per CTA
-// then, and their costs average out.
+// than kDealSeqs of them are dealt as they come, which costs where they are
+// short: 101 pairs of 10 to 200 queries on 20 to 400 keys take 142 us forward
+// and 486 backward where 100 take 123 and 359 (32/8 heads, d = 128; 16/16 heads,
+// d = 64: 85 and 223, 88 and 205).
 #pragma once
 
 #include <cstdint>
