@@ -377,8 +377,8 @@ int fa_decode_shared(const void *q, const void *k_cache, const void *v_cache,
  * of lengths that do not fit, with o bf16.  The keys are split over the whole
  * GPU ("Flash-Decoding"), where fa_fwd_cross gives each 256 rows of a KV head
  * to one SM: the faster call while those leave many SMs idle and the keys are
- * many (30 queries, 16 heads, 4,000 keys 19 us against 62), or for a few tokens
- * (12 sequences of one, 16 heads, 3,000 keys 33 us against 94).
+ * many (30 queries, 16 heads of 64, 4,000 keys 20 us against 60), or for a few
+ * tokens (12 sequences of one, 16 heads of 64, 3,000 keys 32 us against 93).
  *   workspace   fa_decode_cross_workspace_bytes(...) bytes, 256-byte aligned,
  *               not to be shared by calls that may overlap on the GPU.
  *   Hq / Hkv at most 128, Nq * Hq / Hkv at most 524288 (else
